@@ -20,7 +20,8 @@ LIBPATH = os.path.join(LIBDIR, LIBNAME)
 BUILD_DIR = os.path.join(os.path.dirname(PKG), "_build")
 
 SOURCES = ["moe_api.cu", "moe_align.cu", "moe_quant.cu", "moe_gemm.cu", "moe_gemm_bs.cu",
-           "moe_gemm_small.cu", "moe_static.cu", "moe_diag.cu"]
+           "moe_gemm_small.cu", "moe_static.cu", "moe_diag.cu", "kv_api.cu", "kv_tables.cu",
+           "kv_append.cu", "kv_attn.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",
@@ -41,7 +42,8 @@ def _stale() -> bool:
         return True
     lib_mtime = os.path.getmtime(LIBPATH)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(os.path.dirname(PKG), "include", "moe_fp8.h"))
+    include = os.path.join(os.path.dirname(PKG), "include")
+    deps += [os.path.join(include, f) for f in ("moe_fp8.h", "moe_kv.h")]
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(d) > lib_mtime for d in deps if os.path.exists(d))
 

@@ -1,0 +1,19 @@
+// Internal declarations of the paged 8-bit cache: limits, kernel parameter blocks and launchers.
+#pragma once
+
+#include "../../include/moe_kv.h"
+#include "moe_internal.h"
+
+namespace moe {
+
+constexpr int kMaxRequests = 4096;
+constexpr int kMaxGroup = 64;          // query heads per key/value head
+
+cudaError_t launch_kv_tables(const moe_kv_tables_args& a, cudaStream_t s);
+cudaError_t launch_rope_table(float* table, int max_pos, int rot, double base, int scaling,
+                              double factor, double low, double high, int original_len,
+                              float magnitude, cudaStream_t s);
+cudaError_t launch_rope_append(const moe_rope_append_args& a, cudaStream_t s);
+cudaError_t launch_attn_simple(const moe_kv_attention_args& a, cudaStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,253 @@
+"""Binding of include/moe_kv.h: the paged 8-bit key/value cache, its tables, the rotary write and the
+attention that reads it.  As in the rest of the package these functions only marshal arguments; the
+work is done by the library's CUDA kernels on `stream` (default: torch's current stream).
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import NamedTuple
+
+from . import MOE_ERR_INVALID_ARG, SCALE_FP32, MoeError, _check, _stream, load_library
+
+ROPE_HALF = 0
+ROPE_INTERLEAVED = 1
+ROPE_SCALE_NONE = 0
+ROPE_SCALE_LINEAR = 1
+ROPE_SCALE_RAMP = 2
+PAGE_SIZES = (16, 32, 64, 128)
+
+_VP, _SZ, _I, _L, _F, _D = (ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64,
+                            ctypes.c_float, ctypes.c_double)
+
+
+class KVTablesArgs(ctypes.Structure):
+    _fields_ = [(n, _VP) for n in (
+        "cur_len", "new_len", "block_table", "free_list", "free_count", "out_block_table",
+        "out_free_list", "out_free_count", "kv_len", "tok_start", "slot", "position", "request",
+        "run_tok", "run_len", "info")] + [(n, _I) for n in (
+            "B", "max_pages", "num_pages", "page_size", "max_tokens", "max_runs")]
+
+
+class RopeAppendArgs(ctypes.Structure):
+    _fields_ = [(n, _VP) for n in (
+        "q", "k", "v", "q_out", "rope", "position", "slot", "run_tok", "run_len", "k_codes", "v_codes",
+        "k_scale", "v_scale")] + [(n, _L) for n in (
+            "q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride", "v_token_stride",
+            "v_head_stride", "qo_token_stride", "qo_head_stride")] + [(n, _I) for n in (
+                "T", "Hq", "Hkv", "D", "page_size", "num_pages", "max_runs", "rot_dim", "max_pos",
+                "layout", "scale_fmt")]
+
+
+class KVAttentionArgs(ctypes.Structure):
+    _fields_ = [(n, _VP) for n in (
+        "q", "k_codes", "v_codes", "k_scale", "v_scale", "block_table", "kv_len", "tok_start",
+        "out")] + [(n, _L) for n in (
+            "q_token_stride", "q_head_stride", "out_token_stride", "out_head_stride")] + [
+                (n, _I) for n in ("T", "B", "Hq", "Hkv", "D", "page_size", "num_pages", "max_pages",
+                                  "max_q", "window")] + [("sm_scale", _F)]
+
+
+SIGNATURES = {
+    "moe_kv_tables": (_I, [ctypes.POINTER(KVTablesArgs), _VP]),
+    "moe_rope_table": (_I, [_VP, _I, _I, _D, _I, _D, _D, _D, _I, _F, _VP]),
+    "moe_rope_append": (_I, [ctypes.POINTER(RopeAppendArgs), _VP]),
+    "moe_kv_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "moe_kv_attention": (_I, [ctypes.POINTER(KVAttentionArgs), _VP, _SZ, _VP]),
+}
+
+
+class KVTables(NamedTuple):
+    """One step's tables (int32 device tensors), as moe_kv_tables writes them."""
+    block_table: object   # [B, max_pages]
+    free_list: object     # [num_pages]
+    free_count: object    # [1]
+    kv_len: object        # [B]
+    tok_start: object     # [B + 1]
+    slot: object          # [max_tokens]
+    position: object      # [max_tokens]
+    request: object       # [max_tokens]
+    run_tok: object       # [max_runs]
+    run_len: object       # [max_runs]
+    info: object          # [4] added tokens, runs, refused requests, granted pages
+
+
+class KVCache(NamedTuple):
+    """The cache's four tensors: codes uint8 (or float8_e4m3fn) [num_pages, Hkv, page_size, D], scales
+    fp32 [num_pages, Hkv]."""
+    k_codes: object
+    v_codes: object
+    k_scale: object
+    v_scale: object
+
+
+def _bad(what: str):
+    raise MoeError(MOE_ERR_INVALID_ARG, what)
+
+
+def _i32(name: str, t, shape):
+    import torch
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        _bad(f"{name}: a contiguous int32 tensor of shape {shape} is needed")
+    return t.data_ptr()
+
+
+def max_runs(max_tokens: int, page_size: int, num_requests: int) -> int:
+    """A capacity of the run list that always suffices."""
+    return min(max_tokens, max_tokens // page_size + 2 * num_requests)
+
+
+def alloc_kv_cache(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int,
+                   device="cuda") -> KVCache:
+    import torch
+    shape = (num_pages, num_kv_heads, page_size, head_dim)
+    code = [torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2)]
+    scale = [torch.zeros(shape[:2], dtype=torch.float32, device=device) for _ in range(2)]
+    return KVCache(*code, *scale)
+
+
+def alloc_kv_tables(num_requests: int, max_pages: int, num_pages: int, page_size: int,
+                    max_tokens: int, device="cuda") -> KVTables:
+    """A set of tables for `num_requests` requests and steps of up to `max_tokens` tokens: all pages
+    free, no request holds any."""
+    import torch
+    i32 = dict(dtype=torch.int32, device=device)
+    runs = max_runs(max_tokens, page_size, num_requests)
+    return KVTables(
+        block_table=torch.full((num_requests, max_pages), -1, **i32),
+        free_list=torch.arange(num_pages, **i32), free_count=torch.full((1,), num_pages, **i32),
+        kv_len=torch.zeros(num_requests, **i32), tok_start=torch.zeros(num_requests + 1, **i32),
+        slot=torch.full((max_tokens,), -1, **i32), position=torch.zeros(max_tokens, **i32),
+        request=torch.full((max_tokens,), -1, **i32), run_tok=torch.zeros(runs, **i32),
+        run_len=torch.zeros(runs, **i32), info=torch.zeros(4, **i32))
+
+
+def kv_tables(cur_len, new_len, block_table, free_list, free_count, *, page_size: int,
+              max_tokens: int | None = None, out: KVTables | None = None, stream=None) -> KVTables:
+    """Block tables, free stack, slot map and page runs that take the requests from cur_len to new_len
+    cached tokens (moe_kv_tables).  The inputs are left as they are; `out` is the second set of tables
+    (allocated for `max_tokens` added tokens when it is not given)."""
+    B, W = block_table.shape
+    N = free_list.shape[0]
+    if out is None:
+        if max_tokens is None:
+            _bad("kv_tables: max_tokens or out is needed")
+        out = alloc_kv_tables(B, W, N, page_size, max_tokens, block_table.device)
+    T, R = out.slot.shape[0], out.run_tok.shape[0]
+    if max_tokens is not None and max_tokens != T:
+        _bad("kv_tables: out holds another number of tokens than max_tokens")
+    a = KVTablesArgs(
+        _i32("cur_len", cur_len, (B,)), _i32("new_len", new_len, (B,)),
+        _i32("block_table", block_table, (B, W)), _i32("free_list", free_list, (N,)),
+        _i32("free_count", free_count, (1,)), _i32("out.block_table", out.block_table, (B, W)),
+        _i32("out.free_list", out.free_list, (N,)), _i32("out.free_count", out.free_count, (1,)),
+        _i32("out.kv_len", out.kv_len, (B,)), _i32("out.tok_start", out.tok_start, (B + 1,)),
+        _i32("out.slot", out.slot, (T,)), _i32("out.position", out.position, (T,)),
+        _i32("out.request", out.request, (T,)), _i32("out.run_tok", out.run_tok, (R,)),
+        _i32("out.run_len", out.run_len, (R,)), _i32("out.info", out.info, (4,)),
+        B, W, N, page_size, T, R)
+    _check(load_library().moe_kv_tables(ctypes.byref(a), _stream(stream)), "moe_kv_tables")
+    return out
+
+
+def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, *, scaling: int = ROPE_SCALE_NONE,
+               factor: float = 1.0, low: float = 1.0, high: float = 32.0, original_len: int = 4096,
+               magnitude: float = 1.0, out=None, device="cuda", stream=None):
+    """cos and sin of every position, fp32 [max_pos, rot_dim / 2, 2] (moe_rope_table)."""
+    import torch
+    if out is None:
+        out = torch.empty((max_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
+    elif out.dtype != torch.float32 or tuple(out.shape) != (max_pos, rot_dim // 2, 2) or not out.is_contiguous():
+        _bad("rope_table: out is a contiguous fp32 tensor [max_pos, rot_dim / 2, 2]")
+    _check(load_library().moe_rope_table(out.data_ptr(), max_pos, rot_dim, base, scaling, factor, low,
+                                         high, original_len, magnitude, _stream(stream)),
+           "moe_rope_table")
+    return out
+
+
+def _heads(name: str, t, T: int, H: int, D: int):
+    """Pointer, token stride and head stride of a BF16 tensor [T, H, D] with contiguous heads."""
+    import torch
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, H, D) or (t.stride(2) != 1 and t.numel()):
+        _bad(f"{name}: a bfloat16 tensor of shape {(T, H, D)} with contiguous heads is needed")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _cache(cache: KVCache):
+    """Pointers of the cache's tensors and (num_pages, Hkv, page_size, D)."""
+    import torch
+    kc, vc, ks, vs = cache
+    shape = tuple(kc.shape)
+    if (len(shape) != 4 or tuple(vc.shape) != shape or kc.element_size() != 1 or vc.element_size() != 1
+            or tuple(ks.shape) != shape[:2] or tuple(vs.shape) != shape[:2]
+            or ks.dtype != torch.float32 or vs.dtype != torch.float32
+            or not (kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous())):
+        _bad("cache: contiguous codes [num_pages, Hkv, page_size, D] and fp32 scales [num_pages, Hkv] are needed")
+    return (kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr()), shape
+
+
+def rope_append(q, k, v, rope, tables: KVTables, cache: KVCache, *, layout: int = ROPE_HALF,
+                scale_fmt: int = SCALE_FP32, q_out=None, stream=None):
+    """Rotate q and k [T, heads, D] by the tables' positions, write k and v to the cache and return the
+    rotated q (moe_rope_append).  rope: rope_table's result, or None for no rotation; q None: cache
+    write only; q_out may be q.  T is the tables' token capacity."""
+    import torch
+    (kc, vc, ks, vs), (N, Hkv, P, D) = _cache(cache)
+    T, R = tables.slot.shape[0], tables.run_tok.shape[0]
+    rot = max_pos = 0
+    rp = None
+    if rope is not None:
+        if rope.dtype != torch.float32 or rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous():
+            _bad("rope: a contiguous fp32 tensor [max_pos, rot_dim / 2, 2] is needed")
+        max_pos, rot, rp = rope.shape[0], 2 * rope.shape[1], rope.data_ptr()
+    Hq = qp = op = qt = qh = ot = oh = 0
+    if q is not None:
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        qp, qt, qh = _heads("q", q, T, Hq, D)
+        op, ot, oh = _heads("q_out", q_out, T, Hq, D)
+    kp, kt, kh = _heads("k", k, T, Hkv, D)
+    vp, vt, vh = _heads("v", v, T, Hkv, D)
+    a = RopeAppendArgs(qp, kp, vp, op, rp, _i32("position", tables.position, (T,)),
+                       _i32("slot", tables.slot, (T,)), _i32("run_tok", tables.run_tok, (R,)),
+                       _i32("run_len", tables.run_len, (R,)), kc, vc, ks, vs, qt, qh, kt, kh, vt, vh,
+                       ot, oh, T, Hq, Hkv, D, P, N, R, rot, max_pos, layout, scale_fmt)
+    _check(load_library().moe_rope_append(ctypes.byref(a), _stream(stream)), "moe_rope_append")
+    return q_out
+
+
+def kv_attention_workspace_bytes(num_heads: int, num_kv_heads: int, head_dim: int, max_q: int) -> int:
+    return load_library().moe_kv_attention_workspace_bytes(num_heads, num_kv_heads, head_dim, max_q)
+
+
+def alloc_kv_attention_workspace(num_heads: int, num_kv_heads: int, head_dim: int, max_q: int,
+                                 device="cuda"):
+    """A zeroed workspace for kv_attention calls with these heads and up to max_q tokens a request."""
+    import torch
+    n = kv_attention_workspace_bytes(num_heads, num_kv_heads, head_dim, max_q)
+    return torch.zeros(max(256, n), dtype=torch.uint8, device=device)
+
+
+def kv_attention(q, cache: KVCache, block_table, kv_len, tok_start, workspace, *, max_q: int,
+                 sm_scale: float | None = None, window: int = 0, out=None, stream=None):
+    """Causal attention of q [T, Hq, D] over the cache (moe_kv_attention): the tokens of request b are
+    rows [tok_start[b], tok_start[b+1]) of q and the last ones of its kv_len[b] cached tokens.  max_q
+    bounds the tokens of one request; sm_scale defaults to D^-0.5; window > 0 limits how far back a
+    token sees."""
+    import torch
+    (kc, vc, ks, vs), (N, Hkv, P, D) = _cache(cache)
+    T, Hq = q.shape[0], q.shape[1]
+    B, W = block_table.shape
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    qp, qt, qh = _heads("q", q, T, Hq, D)
+    op, ot, oh = _heads("out", out, T, Hq, D)
+    a = KVAttentionArgs(qp, kc, vc, ks, vs, _i32("block_table", block_table, (B, W)),
+                        _i32("kv_len", kv_len, (B,)), _i32("tok_start", tok_start, (B + 1,)), op, qt, qh,
+                        ot, oh, T, B, Hq, Hkv, D, P, N, W, max_q, window,
+                        1.0 / math.sqrt(D) if sm_scale is None else sm_scale)
+    _check(load_library().moe_kv_attention(ctypes.byref(a), workspace.data_ptr(), workspace.numel(),
+                                           _stream(stream)), "moe_kv_attention")
+    return out
