@@ -96,7 +96,7 @@ moe_status moe_rope_append(const moe_rope_append_args* a, moe_stream_t stream) {
 size_t moe_kv_attention_workspace_bytes(int Hq, int Hkv, int D, int max_q) {
   if (Hq <= 0 || max_q <= 0 || check_cache(Hkv, D, 16, 0) != MOE_OK) return 0;
   if (Hq % Hkv || Hq / Hkv > kMaxGroup) return 0;
-  return 256;
+  return few_workspace_bytes(D, few_rows(Hq / Hkv, max_q));
 }
 
 moe_status moe_kv_attention(const moe_kv_attention_args* a, void* workspace, size_t workspace_bytes,
@@ -121,7 +121,12 @@ moe_status moe_kv_attention(const moe_kv_attention_args* a, void* workspace, siz
   if (!stride_ok(a->q_token_stride) || !stride_ok(a->q_head_stride) || !stride_ok(a->out_token_stride) ||
       !stride_ok(a->out_head_stride))
     return MOE_ERR_INVALID_ARG;
-  return launched(launch_attn_simple(*a, (cudaStream_t)stream));
+  if (a->num_pages == 0) return MOE_ERR_INVALID_ARG;
+  const int G = a->Hq / a->Hkv, rows = few_rows(G, a->max_q);
+  cudaError_t err = launch_attn_few(*a, rows, workspace, (cudaStream_t)stream);
+  if (err == cudaSuccess && (long long)G * a->max_q > rows)
+    err = launch_attn_simple(*a, rows / G, (cudaStream_t)stream);
+  return launched(err);
 }
 
 }  // extern "C"

@@ -6,7 +6,7 @@
 namespace moe {
 
 template <int kD>
-__global__ void __launch_bounds__(128) k_attn_simple(const moe_kv_attention_args a) {
+__global__ void __launch_bounds__(128) k_attn_simple(const moe_kv_attention_args a, int min_n) {
   constexpr int kV = kD / 32;
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -19,6 +19,7 @@ __global__ void __launch_bounds__(128) k_attn_simple(const moe_kv_attention_args
     else hi = mid;
   }
   const int b = lo, n = a.tok_start[b + 1] - a.tok_start[b];
+  if (n <= min_n) return;
   const int pos = a.kv_len[b] - n + t - a.tok_start[b];
   const int first = a.window > 0 ? max(0, pos - a.window + 1) : 0;
   const int hk = h / (a.Hq / a.Hkv);
@@ -64,11 +65,11 @@ __global__ void __launch_bounds__(128) k_attn_simple(const moe_kv_attention_args
   for (int i = 0; i < kV; ++i) o[i] = (uint16_t)f32_to_bf16_bits(l > 0.0f ? acc[i] / l : 0.0f);
 }
 
-cudaError_t launch_attn_simple(const moe_kv_attention_args& a, cudaStream_t s) {
+cudaError_t launch_attn_simple(const moe_kv_attention_args& a, int min_n, cudaStream_t s) {
   const unsigned grid = (unsigned)(((long long)a.T * a.Hq + 3) / 4);
   if (grid == 0) return cudaSuccess;
-  if (a.D == 128) k_attn_simple<128><<<grid, 128, 0, s>>>(a);
-  else k_attn_simple<64><<<grid, 128, 0, s>>>(a);
+  if (a.D == 128) k_attn_simple<128><<<grid, 128, 0, s>>>(a, min_n);
+  else k_attn_simple<64><<<grid, 128, 0, s>>>(a, min_n);
   return cudaGetLastError();
 }
 

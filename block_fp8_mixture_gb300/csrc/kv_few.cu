@@ -1,0 +1,796 @@
+// Attention over the 8-bit paged cache for few query rows per request: decode and verification.
+//
+// Every live byte of the cache is read once and costs a handful of operations, so HBM is the bound
+// (256 bytes per token and head at D = 128).  The tokens sit on the MMA's M side and the query rows
+// (tokens of the request x heads that share the key/value head, padded to 16, 32 or 64) on its N
+// side, so that one pass over a 128-token tile serves all rows, and the E4M3 codes go from the cache
+// to the tensor cores as they are:
+//   S^T[token][row] = K[token][:] . Q[row][:]          A = K tile, K-major
+//   O^T[d][row]     = sum_token V[token][d] P[row][token]   A = V tile, MN-major
+// What is not 8-bit is split into E4M3 terms on the N side, each with its own column, which keeps the
+// accumulation in fp32 and costs no second read of A: a row of Q, scaled by a power of two, into
+// two terms (the second x 32: 8 bits, absolute error 2^-15 of the largest value), a row of P into
+// three (x 1, x 32, x 1024: 12 bits down to 2^-13 of the running maximum, 8 at 2^-17, 4 at 2^-21).
+// The page's K scale multiplies the score, its V scale the probability, relative to the tile's largest.
+//
+// The units of work, 128-token tiles of (request, head), are dealt out evenly: CTA c takes units
+// [c U / G, (c + 1) U / G) of the flattened list, whatever the lengths (G = CTAs, at most U).  A CTA that holds part of an
+// item leaves its sums, maximum and unscaled output in the workspace, and k_attn_join adds the parts
+// in CTA order, so results do not depend on timing.
+//   warp 0      producer: lane i fetches page i of the tile (TMA), its scales and the tile's bounds
+//   warp 1      MMA issuer
+//   warps 2..   one warpgroup per 16 rows: thread = token for the scores, = d for the output
+// The maximum that scores are taken relative to moves only when a score passes it by 8 x (2^3): then
+// all threads of the warpgroup reduce the tile's maximum and rescale, else a vote is all it costs.
+#include <algorithm>
+
+#include "kv_internal.h"
+#include "moe_device.cuh"
+
+namespace moe {
+
+constexpr int kTile = 128;                 // tokens per tile
+constexpr int kMaxTilePages = 8;           // pages of a tile, at page size 16
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kPScale = 32.0f;           // P = 1 at the running maximum becomes 32 (up to 256)
+constexpr float kGrow = 3.0f;              // log2 by which a score may pass the maximum
+constexpr float kTermStep = 32.0f;         // each further E4M3 term is scaled up by this
+
+template <int kD, int kNR>
+struct FewCfg {
+  static constexpr int WGs = kNR / 16;
+  static constexpr int Threads = 64 + 128 * WGs;
+  static constexpr int HalfBytes = kTile * kD;              // K or V of a tile
+  static constexpr int StageBytes = 2 * HalfBytes;
+  static constexpr int CtasPerSm = kNR == 16 ? 2 : 1;
+  static constexpr int Stages = (kNR == 16 ? 3 : 5) * (128 / kD);
+  static constexpr int QBytes = 2 * kNR * kD;
+  static constexpr int PBytes = 3 * kNR * kTile;
+  static constexpr int SCols = 2 * kNR;                     // per score buffer, two of them
+  static constexpr int OCol = 2 * SCols;
+  static constexpr int TmemCols = kNR == 16 ? 128 : kNR == 32 ? 256 : 512;
+  static constexpr int SlotBytes = 128;
+  static constexpr int CtrlBytes = 1024 + Stages * SlotBytes + WGs * 5 * 16 * 4;
+  static constexpr int Smem = 1024 + Stages * StageBytes + QBytes + PBytes + CtrlBytes;
+  static_assert(OCol + 3 * kNR <= TmemCols, "tensor memory");
+  static_assert(CtasPerSm * (Smem + 1024) <= 228 * 1024, "shared memory");
+};
+
+// What the softmax warps need of a tile.
+struct FewSlot {
+  float kf[kMaxTilePages];     // K scale x sm_scale x log2 e
+  float vr[kMaxTilePages];     // V scale / vref x kPScale
+  float vref;
+  int token0;                  // first token of the tile
+  int lo, hi;                  // tokens that some row sees
+  int pos0, rows, q0, head;    // position of query token 0, live rows, row of it in q, key/value head
+  int flags;                   // 2: last tile of the segment (of this CTA's part of the item)
+  int part;                    // workspace part that the segment fills, -1: the whole item is here
+  int pad[6];
+};
+static_assert(sizeof(FewSlot) == 128, "slot");
+
+struct FewParams {
+  moe_kv_attention_args a;
+  int G;                       // query heads per key/value head
+  int page_shift;
+  float* parts;                // [2 * gridDim.x][kNR * (kD + 2)]
+  int4* meta;                  // [gridDim.x] item that the CTA continues, item that it leaves open and
+                               // the part that holds it (-1: none)
+  int* status;
+};
+
+// Lengths of request b: cached tokens, query tokens, whether this kernel handles it, and the tiles
+// that hold the tokens its rows see (one, empty, when they see nothing).
+struct FewItem {
+  int L, n, q0, lo, hi, tile0, tiles;
+};
+
+template <int kNR>
+__device__ __forceinline__ FewItem few_item(const FewParams& p, int b) {
+  FewItem it;
+  it.q0 = p.a.tok_start[b];
+  it.n = p.a.tok_start[b + 1] - it.q0;
+  it.L = min(max(p.a.kv_len[b], 0), p.a.max_pages << p.page_shift);
+  it.lo = it.hi = it.tile0 = it.tiles = 0;
+  if (it.n >= 1 && it.n <= kNR / p.G && it.q0 >= 0 && it.q0 + it.n <= p.a.T) {
+    it.hi = it.L;
+    if (p.a.window > 0) it.lo = max(0, it.L - it.n - p.a.window + 1);
+    it.tile0 = it.lo / kTile;
+    it.tiles = max(1, (it.hi + kTile - 1) / kTile - it.tile0);
+  }
+  return it;
+}
+
+// Position in the CTA's units.
+template <int kNR>
+struct FewWalk {
+  int b, h, tile;
+  FewItem item;
+  long long left;              // units from here to the CTA's end
+  __device__ __forceinline__ void next(const FewParams& p) {
+    if (--left <= 0) return;
+    if (++tile < item.tiles) return;
+    tile = 0;
+    if (++h < p.a.Hkv) return;
+    h = 0;
+    do {
+      item = few_item<kNR>(p, ++b);
+    } while (item.tiles == 0 && b < p.a.B - 1);
+  }
+};
+
+__device__ __forceinline__ bool vote_any(int barrier, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "r"(barrier)
+      : "memory");
+  return r != 0;
+}
+
+// 16 values per lane -> the reduction over the warp of value r = lane >> 1 (both lanes of a pair).
+template <bool kMax>
+__device__ __forceinline__ float warp_reduce16(float (&v)[16], int lane) {
+#pragma unroll
+  for (int half = 8; half >= 1; half >>= 1) {
+    const int d = 2 * half;
+    const bool up = lane & d;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+      const float got = __shfl_xor_sync(~0u, send, d);
+      v[i] = kMax ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  const float got = __shfl_xor_sync(~0u, v[0], 1);
+  return kMax ? fmaxf(v[0], got) : v[0] + got;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void e4m3x2_to_f32(uint32_t codes, float& lo, float& hi) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)codes));
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(h2));
+}
+
+__device__ __forceinline__ void st_u8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Offset of byte x of row r in K-major rows of kRow bytes with the 128- or 64-byte swizzle.
+template <int kRow>
+__device__ __forceinline__ uint32_t swz(int r, int x) {
+  const int key = kRow == 128 ? (r & 7) : ((r >> 1) & 3);
+  return (uint32_t)(r * kRow + ((((x >> 4) ^ key) << 4) | (x & 15)));
+}
+
+// Descriptor of rows of kRow bytes (128- or 64-byte swizzle), 8-row groups one after another.  For the
+// MN-major V tile the 8-row groups follow along the reduction axis at the same offset.
+template <int kRow>
+__device__ __forceinline__ uint64_t few_desc(uint32_t saddr) {
+  uint64_t d = make_sdesc_sw128(saddr, 8 * kRow);
+  if (kRow == 64) d = (d & ~((uint64_t)7 << 61)) | ((uint64_t)4 << 61);
+  return d;
+}
+
+template <int kD, int kNR>
+__global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::CtasPerSm)
+    k_attn_few(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+               const __grid_constant__ FewParams p) {
+  using C = FewCfg<kD, kNR>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  uint8_t* ctrl = smem + C::Stages * C::StageBytes + C::QBytes + C::PBytes;
+  const uint32_t sQ = sbase + C::Stages * C::StageBytes, sP = sQ + C::QBytes;
+  FewSlot* slots = reinterpret_cast<FewSlot*>(ctrl + 1024);
+  float* red = reinterpret_cast<float*>(ctrl + 1024 + C::Stages * C::SlotBytes);   // [WGs][5][16]
+  const uint32_t bar0 = smem_addr(ctrl);
+  auto kfull = [&](int s) { return bar0 + 8u * s; };
+  auto vfull = [&](int s) { return bar0 + 8u * (C::Stages + s); };
+  auto ifull = [&](int s) { return bar0 + 8u * (2 * C::Stages + s); };
+  auto empty = [&](int s) { return bar0 + 8u * (3 * C::Stages + s); };
+  constexpr int kB = 4 * C::Stages;
+  auto sfull = [&](int b) { return bar0 + 8u * (kB + b); };
+  const uint32_t qfull = bar0 + 8u * (kB + 2), pfull = bar0 + 8u * (kB + 3), ofull = bar0 + 8u * (kB + 4);
+  const uint32_t drain = bar0 + 8u * (kB + 5);
+  static_assert(8 * (kB + 6) + 160 <= 1024, "barriers");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (kB + 6));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* mma_done = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  long long* scan = reinterpret_cast<long long*>(ctrl + 8 * (kB + 6) + 16);   // [warps + 2]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* status = p.status;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::Stages; ++s) {
+      mbar_init(kfull(s), 1);
+      mbar_init(vfull(s), 1);
+      mbar_init(ifull(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(sfull(0), 1);
+    mbar_init(sfull(1), 1);
+    mbar_init(qfull, 4 * C::WGs);
+    mbar_init(pfull, 4 * C::WGs);
+    mbar_init(ofull, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *mma_done = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  if (warp == 1) tmem_alloc(smem_addr(tmem_slot), C::TmemCols);
+
+  // ------------------------------------------------------------ the CTA's share of the units
+  // units of request b: Hkv x tiles; an exclusive sum over threads with consecutive requests each
+  grid_dep_wait();
+  const int per = (p.a.B + C::Threads - 1) / C::Threads;
+  const int rb0 = threadIdx.x * per, rb1 = min(p.a.B, rb0 + per);
+  long long mine = 0;
+  for (int b = rb0; b < rb1; ++b) mine += (long long)few_item<kNR>(p, b).tiles * p.a.Hkv;
+  long long pre = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long t = __shfl_up_sync(~0u, pre, d);
+    if (lane >= d) pre += t;
+  }
+  constexpr int kWarps = C::Threads / 32;
+  static_assert(8 * (kWarps + 2) <= 160, "scan area");
+  if (lane == 31) scan[warp] = pre;
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  long long total = 0;
+  pre -= mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) pre += scan[w];
+    total += scan[w];
+  }
+  // no more CTAs than units, so the CTAs that share an item are neighbours
+  const long long ctas = min((long long)gridDim.x, total), c = blockIdx.x;
+  const long long u0 = c < ctas ? total * c / ctas : 0, u1 = c < ctas ? total * (c + 1) / ctas : 0;
+  if (u0 < u1 && u0 >= pre && u0 < pre + mine) {
+    long long at = pre;
+    for (int b = rb0; b < rb1; ++b) {
+      const FewItem it = few_item<kNR>(p, b);
+      const long long w = (long long)it.tiles * p.a.Hkv;
+      if (u0 < at + w) {
+        scan[kWarps] = b;
+        scan[kWarps + 1] = u0 - at;
+        break;
+      }
+      at += w;
+    }
+  }
+  __syncthreads();
+  const int units = (int)(u1 - u0);
+  const int first_b = (int)scan[kWarps];
+  const int first_u = (int)scan[kWarps + 1];
+
+  int issued = 0;
+  if (units > 0) {
+    if (warp == 0) {
+      // -------------------------------------------------------------------- producer
+      FewWalk<kNR> cur;
+      cur.b = first_b;
+      cur.item = few_item<kNR>(p, first_b);
+      cur.h = first_u / cur.item.tiles;
+      cur.tile = first_u - cur.h * cur.item.tiles;
+      cur.left = units;
+      const int npg = kTile >> p.page_shift, P = 1 << p.page_shift;
+      // lane i: entry of page i of the tile; -1 where the tile needs none
+      auto entry = [&](const FewWalk<kNR>& w) {
+        if (w.left <= 0 || lane >= npg) return -1;
+        const int pg = (w.item.tile0 + w.tile) * npg + lane;
+        if ((pg << p.page_shift) >= w.item.hi || ((pg + 1) << p.page_shift) <= w.item.lo) return -1;
+        return p.a.block_table[(size_t)w.b * p.a.max_pages + pg];
+      };
+      auto scales = [&](const FewWalk<kNR>& w, int page, float& ks, float& vs) {
+        ks = vs = 0.0f;
+        if (page >= 0 && page < p.a.num_pages) {
+          ks = p.a.k_scale[(size_t)page * p.a.Hkv + w.h];
+          vs = p.a.v_scale[(size_t)page * p.a.Hkv + w.h];
+        }
+      };
+      // entries two tiles ahead, scales one
+      FewWalk<kNR> nxt = cur, far;
+      int page = entry(cur);
+      nxt.next(p);
+      int page1 = entry(nxt);
+      far = nxt;
+      far.next(p);
+      float ks, vs;
+      scales(cur, page, ks, vs);
+      int head_item = -1, tail_item = -1, tail_part = -1, seg = 0;
+      bool first = true;
+      for (int it = 0; it < units; ++it) {
+        const int page2 = entry(far);
+        float ks1, vs1;
+        scales(nxt, page1, ks1, vs1);
+        const int s = it % C::Stages;
+        bool ok = true;
+        if (lane == 0) ok = mbar_wait(empty(s), ((it / C::Stages) & 1) ^ 1, abort_flag, status);
+        if (!__shfl_sync(~0u, (int)ok, 0)) break;
+        const bool live = page >= 0 && page < p.a.num_pages;
+        const uint32_t bytes = __popc(__ballot_sync(~0u, live)) * P * kD;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(kfull(s), bytes);
+          mbar_arrive_expect_tx(vfull(s), bytes);
+        }
+        __syncwarp();
+        const uint32_t dst = sbase + s * C::StageBytes + lane * P * kD;
+        if (live) {
+          tma_load_4d(dst, &tmK, 0, 0, cur.h, page, kfull(s));
+          tma_load_4d(dst + C::HalfBytes, &tmV, 0, 0, cur.h, page, vfull(s));
+        }
+        float vref = live ? vs : 0.0f;
+#pragma unroll
+        for (int d = 4; d; d >>= 1) vref = fmaxf(vref, __shfl_xor_sync(~0u, vref, d));
+        FewSlot& slot = slots[s];
+        if (lane < npg) {
+          slot.kf[lane] = ks * p.a.sm_scale * kLog2e;
+          slot.vr[lane] = vref > 0.0f ? __fdiv_rn(vs, vref) * kPScale : (vs == vs ? 0.0f : vs);
+        }
+        if (lane == 0) {
+          const bool begin = cur.tile == 0, end = cur.tile == cur.item.tiles - 1;
+          const bool last = cur.left == 1;
+          const int item = cur.b * p.a.Hkv + cur.h;
+          slot.vref = vref;
+          slot.token0 = (cur.item.tile0 + cur.tile) * kTile;
+          slot.lo = cur.item.lo;
+          slot.hi = cur.item.hi;
+          slot.pos0 = cur.item.L - cur.item.n;
+          slot.rows = cur.item.n * p.G;
+          slot.q0 = cur.item.q0;
+          slot.head = cur.h;
+          slot.flags = end || last ? 2 : 0;
+          if (first && !begin) head_item = item;
+          // the segment's part of the workspace; an item that lies wholly in this CTA needs none
+          const int part = 2 * (int)blockIdx.x + (seg > 0 ? 1 : 0);
+          slot.part = end && head_item != item ? -1 : part;
+          if (last && !end && head_item != item) {
+            tail_item = item;
+            tail_part = part;
+          }
+          mbar_arrive(ifull(s));
+        }
+        if (cur.tile == cur.item.tiles - 1) ++seg;
+        first = false;
+        ++issued;
+        cur = nxt;
+        nxt = far;
+        far.next(p);
+        page = page1;
+        page1 = page2;
+        ks = ks1;
+        vs = vs1;
+      }
+      if (lane == 0) p.meta[blockIdx.x] = make_int4(head_item, tail_item, tail_part, 0);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------------------- MMA
+      if (lane == 0) {
+        constexpr uint32_t kIdescS = make_idesc_e4m3(kTile, 2 * kNR);
+        constexpr uint32_t kIdescO = make_idesc_e4m3(kD, 3 * kNR) | (1u << 15);   // A = V^T: MN-major
+        const uint64_t qd = few_desc<kD>(sQ), pd = few_desc<128>(sP);
+        int segs = 0;
+        bool ok = true;
+        auto scores = [&](int it) {
+          const int s = it % C::Stages;
+          if (!mbar_wait(kfull(s), (it / C::Stages) & 1, abort_flag, status)) return false;
+          tc_fence_after_sync();
+          const uint64_t kd = few_desc<kD>(sbase + s * C::StageBytes);
+          const uint32_t d = tmem + (it & 1) * C::SCols;
+#pragma unroll
+          for (int k = 0; k < kD / 32; ++k) mma_f8(d, kd + 2 * k, qd + 2 * k, kIdescS, k > 0);
+          mma_commit(sfull(it & 1));
+          return true;
+        };
+        for (int it = 0; ok && it < units; ++it) {
+          const int s = it % C::Stages;
+          // the slot of tile it + 1 may not be there yet; only its segment flag is needed
+          if (it == 0) {
+            if (!mbar_wait(qfull, segs & 1, abort_flag, status) || !scores(0)) break;
+            ++segs;
+          }
+          if (!mbar_wait(ifull(s), (it / C::Stages) & 1, abort_flag, status)) break;
+          const int flags = *reinterpret_cast<volatile int*>(&slots[s].flags);
+          const bool more = it + 1 < units, same = !(flags & 2);
+          if (more && same && !scores(it + 1)) break;
+          if (!mbar_wait(pfull, it & 1, abort_flag, status) ||
+              !mbar_wait(vfull(s), (it / C::Stages) & 1, abort_flag, status))
+            break;
+          tc_fence_after_sync();
+          const uint32_t sv = sbase + s * C::StageBytes + C::HalfBytes;
+#pragma unroll
+          for (int k = 0; k < kTile / 32; ++k)
+            mma_f8(tmem + C::OCol, few_desc<kD>(sv + k * 32 * kD), pd + 2 * k, kIdescO, k > 0);
+          mma_commit(ofull);
+          mma_commit(empty(s));
+          *mma_done = it + 1;
+          if (more && !same) {
+            if (!mbar_wait(qfull, segs & 1, abort_flag, status) || !scores(it + 1)) break;
+            ++segs;
+          }
+        }
+      }
+    } else {
+      // --------------------------------------------------------------------- softmax
+      const int wg = (warp - 2) >> 2, q = warp & 3;
+      const int tl = q * 32 + lane;                     // token of the tile
+      const int wt = (warp - 2 - 4 * wg) * 32 + lane;   // thread of the warpgroup, for Q
+      const bool holds_d = kD == 128 || lane < 16;
+      const int d = kD == 128 ? tl : q * 16 + lane;     // output column of this thread
+      float* wred = red + wg * 80;                      // [4 warps][16 rows], for reductions
+      float* wqs = wred + 64;                           // [16 rows] value of a code of Q
+      const int r0 = wg * 16;
+      float m[16], l[16], acc[16];
+      float vref_prev = 0.0f;
+      // A wait that runs out only marks the thread: the warpgroup leaves together, at the next vote,
+      // so no barrier is left waiting.
+      bool pending = false, bad = false, begin = true;
+      auto add_output = [&](int it) {                   // O of tile it
+        if (!mbar_wait(ofull, it & 1, abort_flag, status)) {
+          bad = true;
+          return;
+        }
+        tc_fence_after_sync();
+        uint32_t t[16];
+        const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + C::OCol + r0;
+        float f = vref_prev * (1.0f / kPScale);
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {
+          tmem_ld16(at + term * kNR, t);
+          tmem_ld_wait();
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[r] = __fmaf_rn(__uint_as_float(t[r]), f, acc[r]);
+          f *= 1.0f / kTermStep;
+        }
+        tc_fence_before_sync();
+      };
+      for (int it = 0; it < units; ++it) {
+        const int s = it % C::Stages;
+        if (!mbar_wait(ifull(s), (it / C::Stages) & 1, abort_flag, status)) bad = true;
+        const FewSlot& slot = slots[s];
+        const int rows = bad ? 0 : slot.rows, pos0 = slot.pos0, q0 = slot.q0, head = slot.head;
+        if (begin) {
+          // the segment's rows of Q: 8 threads a row, D / 8 values each, two E4M3 terms
+          constexpr int kV = kD / 8;
+          const int r = r0 + (wt >> 3), c = wt & 7;
+          float x[kV];
+#pragma unroll
+          for (int i = 0; i < kV; ++i) x[i] = 0.0f;
+          if (r < rows) {
+            const int i = r / p.G;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                static_cast<const uint16_t*>(p.a.q) + (int64_t)(q0 + i) * p.a.q_token_stride +
+                (int64_t)(head * p.G + r - i * p.G) * p.a.q_head_stride + c * kV);
+#pragma unroll
+            for (int v = 0; v < kV / 8; ++v) {
+              const uint4 w = src[v];
+              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                x[8 * v + 2 * j] = __uint_as_float(u[j] << 16);
+                x[8 * v + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+              }
+            }
+          }
+          float amax = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kV; ++i) amax = fmaxf(amax, fabsf(x[i]));
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+          // amax x mul in [128, 256)
+          const int e = amax > 0.0f ? max((int)(__float_as_uint(amax) >> 23) - 127, -100) : 0;
+          const float mul = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+          uint32_t t1[kV / 4], t2[kV / 4];
+#pragma unroll
+          for (int i = 0; i < kV / 4; ++i) {
+            t1[i] = t2[i] = 0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float a = x[4 * i + 2 * j] * mul, b = x[4 * i + 2 * j + 1] * mul;
+              const uint32_t code = cvt_e4m3x2(a, b);
+              float fa, fb;
+              e4m3x2_to_f32(code, fa, fb);
+              t1[i] |= code << (16 * j);
+              t2[i] |= cvt_e4m3x2((a - fa) * kTermStep, (b - fb) * kTermStep) << (16 * j);
+            }
+          }
+          uint8_t* qb = smem + C::Stages * C::StageBytes;
+#pragma unroll
+          for (int i = 0; i < kV / 4; i += 2) {
+            *reinterpret_cast<uint2*>(qb + swz<kD>(r, c * kV + 4 * i)) = make_uint2(t1[i], t1[i + 1]);
+            *reinterpret_cast<uint2*>(qb + swz<kD>(kNR + r, c * kV + 4 * i)) = make_uint2(t2[i], t2[i + 1]);
+          }
+          if (c == 0) wqs[wt >> 3] = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
+          fence_proxy_async_smem();
+          named_barrier_sync(1 + wg, 128);
+          if (lane == 0) mbar_arrive(qfull);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            m[i] = -INFINITY;
+            l[i] = acc[i] = 0.0f;
+          }
+        }
+        // scores of this thread's token
+        const int page = tl >> p.page_shift;
+        const float kf = slot.kf[page], vr = slot.vr[page];
+        const int j = slot.token0 + tl;
+        const bool edge = slot.token0 < slot.lo || slot.token0 + kTile > slot.hi;
+        // rows [from, to) of the warpgroup see the token
+        int from = (j - pos0) * p.G, to = rows;
+        if (p.a.window > 0) to = min(to, j - pos0 + p.a.window > 0 ? (j - pos0 + p.a.window) * p.G : 0);
+        if (j >= slot.hi || j < slot.lo) to = 0;
+        from = min(max(from - r0, 0), 16);
+        to = min(max(to - r0, 0), 16);
+        const uint32_t seen = to > from ? ((1u << to) - (1u << from)) : 0u;
+        if (!mbar_wait(sfull(it & 1), (it >> 1) & 1, abort_flag, status)) bad = true;
+        tc_fence_after_sync();
+        float sc[16];
+        {
+          uint32_t t[16], t2[16];
+          const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (it & 1) * C::SCols + r0;
+          tmem_ld16(at, t);
+          tmem_ld16(at + kNR, t2);
+          tmem_ld_wait();
+          tc_fence_before_sync();
+#pragma unroll
+          for (int r = 0; r < 16; r += 4) {
+            const float4 qs = *reinterpret_cast<const float4*>(wqs + r);
+            const float f[4] = {qs.x * kf, qs.y * kf, qs.z * kf, qs.w * kf};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float v = __fmaf_rn(__uint_as_float(t2[r + i]), 1.0f / kTermStep, __uint_as_float(t[r + i]));
+              sc[r + i] = (seen >> (r + i)) & 1 ? v * f[i] : -INFINITY;
+            }
+          }
+        }
+        bool grow = false;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) grow |= sc[r] > m[r] + kGrow;
+        if (vote_any(1 + wg, grow || bad)) {
+          if (vote_any(1 + wg, bad)) break;
+          // the maximum of some row moved: bring what is outstanding in, then rescale
+          if (pending) add_output(it - 1);
+          pending = false;
+          float v[16];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) v[r] = sc[r];
+          const float top = warp_reduce16<true>(v, lane);
+          if (!(lane & 1)) wred[q * 16 + (lane >> 1)] = top;
+          named_barrier_sync(1 + wg, 128);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float t = fmaxf(fmaxf(wred[r], wred[16 + r]), fmaxf(wred[32 + r], wred[48 + r]));
+            const float mn = fmaxf(m[r], t);
+            const float alpha = m[r] == mn ? 1.0f : exp2_approx(m[r] - mn);
+            l[r] *= alpha;
+            acc[r] *= alpha;
+            m[r] = mn;
+          }
+        }
+        if (pending) add_output(it - 1);
+        // probabilities, three E4M3 terms each; rows two by two
+#pragma unroll
+        for (int r = 0; r < 16; r += 2) {
+          const float p0 = exp2_approx(sc[r] - (m[r] == -INFINITY ? 0.0f : m[r]));
+          const float p1 = exp2_approx(sc[r + 1] - (m[r + 1] == -INFINITY ? 0.0f : m[r + 1]));
+          l[r] += p0;
+          l[r + 1] += p1;
+          float a = p0 * vr, b = p1 * vr;
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {
+            const uint32_t code = cvt_e4m3x2(a, b);
+            const int row = term * kNR + r0 + r;
+            st_u8(sP + swz<128>(row, tl), code);
+            st_u8(sP + swz<128>(row + 1, tl), code >> 8);
+            if (term < 2) {
+              float fa, fb;
+              e4m3x2_to_f32(code, fa, fb);
+              a = (a - fa) * kTermStep;
+              b = (b - fb) * kTermStep;
+            }
+          }
+        }
+        if (edge && wg == 0) {
+          // V rows that no query row sees may hold anything: 0 x NaN would spread
+          if (!mbar_wait(vfull(s), (it / C::Stages) & 1, abort_flag, status)) bad = true;
+          if (j < slot.lo || j >= slot.hi) {
+            uint4* row = reinterpret_cast<uint4*>(smem + s * C::StageBytes + C::HalfBytes + tl * kD);
+#pragma unroll
+            for (int i = 0; i < kD / 16; ++i) row[i] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        vref_prev = slot.vref;
+        pending = true;
+        const int part = slot.part;
+        begin = slot.flags & 2;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull);
+        if (begin) {
+          // ------------------------------------------------------- end of the segment
+          add_output(it);
+          pending = false;
+          const float sum = warp_reduce16<false>(l, lane);
+          if (!(lane & 1)) wred[q * 16 + (lane >> 1)] = sum;
+          named_barrier_sync(1 + wg, 128);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            l[r] = (wred[r] + wred[16 + r]) + (wred[32 + r] + wred[48 + r]);
+            const int row = r0 + r;
+            if (row >= rows || !holds_d) continue;
+            if (part < 0) {
+              const int i = row / p.G;
+              static_cast<uint16_t*>(p.a.out)[(int64_t)(q0 + i) * p.a.out_token_stride +
+                                              (int64_t)(head * p.G + row - i * p.G) * p.a.out_head_stride + d] =
+                  (uint16_t)f32_to_bf16_bits(l[r] > 0.0f || l[r] != l[r] ? acc[r] / l[r] : 0.0f);
+            } else {
+              float* o = p.parts + (size_t)part * (kNR * (kD + 2));
+              o[row * kD + d] = acc[r];
+              if (d == 0) {
+                o[kNR * kD + 2 * row] = m[r];
+                o[kNR * kD + 2 * row + 1] = l[r];
+              }
+            }
+          }
+          named_barrier_sync(1 + wg, 128);     // the sums have been read
+        }
+      }
+    }
+  } else if (threadIdx.x == 0) {
+    p.meta[blockIdx.x] = make_int4(-1, -1, -1, 0);
+  }
+
+  // ------------------------------------------------------------------------ teardown
+  __syncthreads();
+  grid_dep_launch_dependents();
+  auto drain_wait = [&](uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        atomicCAS(status, 0, (int)MOE_ERR_DEVICE_TIMEOUT);
+        return;
+      }
+    }
+  };
+  if (warp == 1 && lane == 0) {
+    mma_commit(drain);
+    drain_wait(drain, 0);
+  }
+  if (warp == 0 && lane == 0 && *abort_flag) {
+    for (int i = *mma_done; i < issued; ++i) {
+      drain_wait(kfull(i % C::Stages), (i / C::Stages) & 1);
+      drain_wait(vfull(i % C::Stages), (i / C::Stages) & 1);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, C::TmemCols);
+  }
+}
+
+// Joins the parts of an item that several CTAs hold.  Block c looks after the item that CTA c leaves
+// open (if any): CTA c's last segment, then the first segments of the CTAs that continue it.
+// blockIdx.y: rows, 4 a block (8 at D = 64).
+template <int kD, int kNR>
+__global__ void __launch_bounds__(128) k_attn_join(const FewParams p, int ctas) {
+  grid_dep_wait();
+  const int c = blockIdx.x;
+  const int4 me = p.meta[c];
+  if (me.y < 0) return;
+  const int b = me.y / p.a.Hkv, h = me.y - b * p.a.Hkv;
+  const int q0 = p.a.tok_start[b], rows = (p.a.tok_start[b + 1] - q0) * p.G;
+  constexpr int kRows = 512 / kD;
+  const int row0 = blockIdx.y * kRows;
+  if (row0 >= rows) return;
+  // parts: this CTA's last segment, then those of CTAs c + 1 .. c + n - 1
+  int n = 1;
+  for (int base = c + 1; base < ctas; base += 128) {
+    const int at = base + threadIdx.x;
+    const int got = __syncthreads_count(at < ctas && p.meta[at].x == me.y);
+    n += got;
+    if (got < 128) break;
+  }
+  constexpr size_t kPart = kNR * (kD + 2);
+  auto part = [&](int i) { return p.parts + (size_t)(i == 0 ? me.z : 2 * (c + i)) * kPart; };
+  const int d = threadIdx.x & (kD - 1);
+  for (int row = row0 + threadIdx.x / kD; row < min(rows, row0 + kRows); row += 128 / kD) {
+    float m = -INFINITY;
+    for (int i = 0; i < n; ++i) m = fmaxf(m, part(i)[kNR * kD + 2 * row]);
+    float l = 0.0f, acc = 0.0f;
+    for (int i = 0; i < n; ++i) {
+      const float* o = part(i);
+      const float mi = o[kNR * kD + 2 * row];
+      const float w = mi == m ? 1.0f : exp2_approx(mi - m);
+      l = __fmaf_rn(o[kNR * kD + 2 * row + 1], w, l);
+      acc = __fmaf_rn(o[row * kD + d], w, acc);
+    }
+    const int i = row / p.G;
+    static_cast<uint16_t*>(p.a.out)[(int64_t)(q0 + i) * p.a.out_token_stride +
+                                    (int64_t)(h * p.G + row - i * p.G) * p.a.out_head_stride + d] =
+        (uint16_t)f32_to_bf16_bits(l > 0.0f || l != l ? acc / l : 0.0f);
+  }
+}
+
+// ------------------------------------------------------------------------------------ launch
+// Rows per item of a call: tokens of a request x heads that share a key/value head, 16, 32 or 64.
+int few_rows(int G, int max_q) {
+  const long long r = (long long)G * max_q;
+  const long long rows = r <= 64 ? r : G;   // prompts: the single tokens among them still come here
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+static int few_ctas(int nr) { return nr == 16 ? 304 : 152; }   // at most; 152 SMs
+
+size_t few_workspace_bytes(int D, int nr) {
+  const int ctas = few_ctas(nr);
+  return 256 + (size_t)ctas * sizeof(int4) + (size_t)2 * ctas * nr * (D + 2) * 4;
+}
+
+static bool cache_map(CUtensorMap* m, const void* codes, int D, int P, int Hkv, int pages) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)P, (cuuint64_t)Hkv, (cuuint64_t)pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)D, (cuuint64_t)P * D, (cuuint64_t)Hkv * P * D};
+  const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)P, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(codes), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kD, int kNR>
+static cudaError_t launch(const moe_kv_attention_args& a, void* workspace, cudaStream_t s) {
+  using C = FewCfg<kD, kNR>;
+  CUtensorMap tmK, tmV;
+  if (!cache_map(&tmK, a.k_codes, kD, a.page_size, a.Hkv, a.num_pages) ||
+      !cache_map(&tmV, a.v_codes, kD, a.page_size, a.Hkv, a.num_pages))
+    return cudaErrorInvalidValue;
+  cudaError_t err = cudaFuncSetAttribute(k_attn_few<kD, kNR>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem);
+  if (err != cudaSuccess) return err;
+  const int ctas = std::min(few_ctas(kNR), sm_count() * C::CtasPerSm);
+  FewParams p;
+  p.a = a;
+  p.G = a.Hq / a.Hkv;
+  p.page_shift = __builtin_ctz((unsigned)a.page_size);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.status = reinterpret_cast<int*>(ws);
+  p.meta = reinterpret_cast<int4*>(ws + 256);
+  p.parts = reinterpret_cast<float*>(ws + 256 + (size_t)few_ctas(kNR) * sizeof(int4));
+  err = launch_pdl(k_attn_few<kD, kNR>, dim3(ctas), dim3(C::Threads), C::Smem, s, tmK, tmV, p);
+  if (err != cudaSuccess) return err;
+  const int rows = std::min<long long>((long long)p.G * a.max_q, kNR);
+  return launch_pdl(k_attn_join<kD, kNR>, dim3(ctas, (rows + 512 / kD - 1) / (512 / kD)), dim3(128), 0, s, p, ctas);
+}
+
+cudaError_t launch_attn_few(const moe_kv_attention_args& a, int nr, void* workspace, cudaStream_t s) {
+  if (a.D == 128)
+    return nr == 16 ? launch<128, 16>(a, workspace, s)
+           : nr == 32 ? launch<128, 32>(a, workspace, s) : launch<128, 64>(a, workspace, s);
+  return nr == 16 ? launch<64, 16>(a, workspace, s)
+         : nr == 32 ? launch<64, 32>(a, workspace, s) : launch<64, 64>(a, workspace, s);
+}
+
+}  // namespace moe

@@ -14,6 +14,11 @@ cudaError_t launch_rope_table(float* table, int max_pos, int rot, double base, i
                               double factor, double low, double high, int original_len,
                               float magnitude, cudaStream_t s);
 cudaError_t launch_rope_append(const moe_rope_append_args& a, cudaStream_t s);
-cudaError_t launch_attn_simple(const moe_kv_attention_args& a, cudaStream_t s);
+// Requests with few query rows: n <= few_rows / (Hq / Hkv) tokens.
+int few_rows(int G, int max_q);
+size_t few_workspace_bytes(int D, int rows);
+cudaError_t launch_attn_few(const moe_kv_attention_args& a, int rows, void* workspace, cudaStream_t s);
+// Requests with more than min_n tokens.
+cudaError_t launch_attn_simple(const moe_kv_attention_args& a, int min_n, cudaStream_t s);
 
 }  // namespace moe

@@ -88,6 +88,14 @@ struct Plan {
   int act_fmt;
 };
 
+// cuTensorMapEncodeTiled, looked up once through the runtime (nullptr when the driver has none).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+int sm_count();                    // of the current device
+
 moe_status make_plan(int M_cap, int E, int H, int I, int topk, int act_fmt, Plan* plan);
 
 // ------------------------------------------------------------ kernel params
