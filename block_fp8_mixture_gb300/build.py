@@ -21,7 +21,7 @@ BUILD_DIR = os.path.join(os.path.dirname(PKG), "_build")
 
 SOURCES = ["moe_api.cu", "moe_align.cu", "moe_quant.cu", "moe_gemm.cu", "moe_gemm_bs.cu",
            "moe_gemm_small.cu", "moe_static.cu", "moe_diag.cu", "kv_api.cu", "kv_tables.cu",
-           "kv_append.cu", "kv_few.cu", "kv_attn.cu"]
+           "kv_append.cu", "kv_few.cu", "kv_prompt.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",

@@ -96,7 +96,9 @@ moe_status moe_rope_append(const moe_rope_append_args* a, moe_stream_t stream) {
 size_t moe_kv_attention_workspace_bytes(int Hq, int Hkv, int D, int max_q) {
   if (Hq <= 0 || max_q <= 0 || check_cache(Hkv, D, 16, 0) != MOE_OK) return 0;
   if (Hq % Hkv || Hq / Hkv > kMaxGroup) return 0;
-  return few_workspace_bytes(D, few_rows(Hq / Hkv, max_q));
+  const int G = Hq / Hkv, rows = few_rows(G, max_q);
+  const size_t few = (few_workspace_bytes(D, rows) + 255) & ~(size_t)255;
+  return (long long)G * max_q > rows ? few + prompt_workspace_bytes(D) : few;
 }
 
 moe_status moe_kv_attention(const moe_kv_attention_args* a, void* workspace, size_t workspace_bytes,
@@ -123,9 +125,14 @@ moe_status moe_kv_attention(const moe_kv_attention_args* a, void* workspace, siz
     return MOE_ERR_INVALID_ARG;
   if (a->num_pages == 0) return MOE_ERR_INVALID_ARG;
   const int G = a->Hq / a->Hkv, rows = few_rows(G, a->max_q);
+  const bool prompts = (long long)G * a->max_q > rows;   // some request may have more rows than that
+  if (prompts && !prompt_fits(a->T, G, a->B)) return MOE_ERR_UNSUPPORTED_SHAPE;
   cudaError_t err = launch_attn_few(*a, rows, workspace, (cudaStream_t)stream);
-  if (err == cudaSuccess && (long long)G * a->max_q > rows)
-    err = launch_attn_simple(*a, rows / G, (cudaStream_t)stream);
+  if (err == cudaSuccess && prompts) {
+    const size_t few = (few_workspace_bytes(a->D, rows) + 255) & ~(size_t)255;
+    err = launch_attn_prompt(*a, rows / G, static_cast<int*>(workspace),
+                             static_cast<uint8_t*>(workspace) + few, (cudaStream_t)stream);
+  }
   return launched(err);
 }
 

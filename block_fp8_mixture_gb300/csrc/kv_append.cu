@@ -9,8 +9,7 @@
 // eight warps, so small pages pack several units into a block.  The remaining blocks rotate Q, 16
 // values per thread: a chunk of 8 pairs (HALF: 8 values and the 8 at rot/2 from them), so that every
 // cos/sin is loaded once per thread.  Bound by HBM: Q in and out, K and V in at 2 bytes, codes out.
-#include "kv_internal.h"
-#include "moe_device.cuh"
+#include "kv_device.cuh"
 
 namespace moe {
 
@@ -80,14 +79,8 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 // Four E4M3 codes times r, rounded back to E4M3.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
   float f[4];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(w >> (16 * h))));
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
-        : "=f"(f[2 * h]), "=f"(f[2 * h + 1])
-        : "r"(h2));
-  }
+  e4m3x2_to_f32(w, f[0], f[1]);
+  e4m3x2_to_f32(w >> 16, f[2], f[3]);
   return codes4(__fmul_rn(f[0], r), __fmul_rn(f[1], r), __fmul_rn(f[2], r), __fmul_rn(f[3], r));
 }
 

@@ -1,0 +1,59 @@
+// What the attention kernels over the paged 8-bit cache share: tiles of 128 tokens, their tensor map and
+// shared-memory layouts, and conversions.
+#pragma once
+
+#include "kv_internal.h"
+#include "moe_device.cuh"
+
+namespace moe {
+
+constexpr int kTile = 128;                 // tokens per tile
+constexpr int kMaxTilePages = 8;           // pages of a tile, at page size 16
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void e4m3x2_to_f32(uint32_t codes, float& lo, float& hi) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)codes));
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(h2));
+}
+
+// Offset of byte x of row r in K-major rows of kRow bytes with the 128- or 64-byte swizzle.
+template <int kRow>
+__device__ __forceinline__ uint32_t swz(int r, int x) {
+  const int key = kRow == 128 ? (r & 7) : ((r >> 1) & 3);
+  return (uint32_t)(r * kRow + ((((x >> 4) ^ key) << 4) | (x & 15)));
+}
+
+// Descriptor of rows of kRow bytes (128- or 64-byte swizzle), 8-row groups one after another.  For the
+// MN-major V tile the 8-row groups follow along the reduction axis at the same offset.
+template <int kRow>
+__device__ __forceinline__ uint64_t rows_desc(uint32_t saddr) {
+  uint64_t d = make_sdesc_sw128(saddr, 8 * kRow);
+  if (kRow == 64) d = (d & ~((uint64_t)7 << 61)) | ((uint64_t)4 << 61);
+  return d;
+}
+
+// The cache's codes as (value, row of the page, head, page); one box is a page of one head, laid out
+// in rows of D bytes with the swizzle of that width.
+inline bool cache_map(CUtensorMap* m, const void* codes, int D, int P, int Hkv, int pages) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)P, (cuuint64_t)Hkv, (cuuint64_t)pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)D, (cuuint64_t)P * D, (cuuint64_t)Hkv * P * D};
+  const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)P, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(codes), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace moe

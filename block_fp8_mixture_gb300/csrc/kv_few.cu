@@ -24,14 +24,10 @@
 // all threads of the warpgroup reduce the tile's maximum and rescale, else a vote is all it costs.
 #include <algorithm>
 
-#include "kv_internal.h"
-#include "moe_device.cuh"
+#include "kv_device.cuh"
 
 namespace moe {
 
-constexpr int kTile = 128;                 // tokens per tile
-constexpr int kMaxTilePages = 8;           // pages of a tile, at page size 16
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPScale = 32.0f;           // P = 1 at the running maximum becomes 32 (up to 256)
 constexpr float kGrow = 3.0f;              // log2 by which a score may pass the maximum
 constexpr float kTermStep = 32.0f;         // each further E4M3 term is scaled up by this
@@ -149,38 +145,8 @@ __device__ __forceinline__ float warp_reduce16(float (&v)[16], int lane) {
   return kMax ? fmaxf(v[0], got) : v[0] + got;
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ void e4m3x2_to_f32(uint32_t codes, float& lo, float& hi) {
-  uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)codes));
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-      : "=f"(lo), "=f"(hi)
-      : "r"(h2));
-}
-
 __device__ __forceinline__ void st_u8(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
-// Offset of byte x of row r in K-major rows of kRow bytes with the 128- or 64-byte swizzle.
-template <int kRow>
-__device__ __forceinline__ uint32_t swz(int r, int x) {
-  const int key = kRow == 128 ? (r & 7) : ((r >> 1) & 3);
-  return (uint32_t)(r * kRow + ((((x >> 4) ^ key) << 4) | (x & 15)));
-}
-
-// Descriptor of rows of kRow bytes (128- or 64-byte swizzle), 8-row groups one after another.  For the
-// MN-major V tile the 8-row groups follow along the reduction axis at the same offset.
-template <int kRow>
-__device__ __forceinline__ uint64_t few_desc(uint32_t saddr) {
-  uint64_t d = make_sdesc_sw128(saddr, 8 * kRow);
-  if (kRow == 64) d = (d & ~((uint64_t)7 << 61)) | ((uint64_t)4 << 61);
-  return d;
 }
 
 template <int kD, int kNR>
@@ -387,14 +353,14 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       if (lane == 0) {
         constexpr uint32_t kIdescS = make_idesc_e4m3(kTile, 2 * kNR);
         constexpr uint32_t kIdescO = make_idesc_e4m3(kD, 3 * kNR) | (1u << 15);   // A = V^T: MN-major
-        const uint64_t qd = few_desc<kD>(sQ), pd = few_desc<128>(sP);
+        const uint64_t qd = rows_desc<kD>(sQ), pd = rows_desc<128>(sP);
         int segs = 0;
         bool ok = true;
         auto scores = [&](int it) {
           const int s = it % C::Stages;
           if (!mbar_wait(kfull(s), (it / C::Stages) & 1, abort_flag, status)) return false;
           tc_fence_after_sync();
-          const uint64_t kd = few_desc<kD>(sbase + s * C::StageBytes);
+          const uint64_t kd = rows_desc<kD>(sbase + s * C::StageBytes);
           const uint32_t d = tmem + (it & 1) * C::SCols;
 #pragma unroll
           for (int k = 0; k < kD / 32; ++k) mma_f8(d, kd + 2 * k, qd + 2 * k, kIdescS, k > 0);
@@ -419,7 +385,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           const uint32_t sv = sbase + s * C::StageBytes + C::HalfBytes;
 #pragma unroll
           for (int k = 0; k < kTile / 32; ++k)
-            mma_f8(tmem + C::OCol, few_desc<kD>(sv + k * 32 * kD), pd + 2 * k, kIdescO, k > 0);
+            mma_f8(tmem + C::OCol, rows_desc<kD>(sv + k * 32 * kD), pd + 2 * k, kIdescO, k > 0);
           mma_commit(ofull);
           mma_commit(empty(s));
           *mma_done = it + 1;
@@ -745,19 +711,6 @@ static int few_ctas(int nr) { return nr == 16 ? 304 : 152; }   // at most; 152 S
 size_t few_workspace_bytes(int D, int nr) {
   const int ctas = few_ctas(nr);
   return 256 + (size_t)ctas * sizeof(int4) + (size_t)2 * ctas * nr * (D + 2) * 4;
-}
-
-static bool cache_map(CUtensorMap* m, const void* codes, int D, int P, int Hkv, int pages) {
-  const EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)P, (cuuint64_t)Hkv, (cuuint64_t)pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)D, (cuuint64_t)P * D, (cuuint64_t)Hkv * P * D};
-  const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)P, 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(codes), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE,
-            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int kD, int kNR>

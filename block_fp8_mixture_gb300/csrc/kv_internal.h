@@ -18,7 +18,10 @@ cudaError_t launch_rope_append(const moe_rope_append_args& a, cudaStream_t s);
 int few_rows(int G, int max_q);
 size_t few_workspace_bytes(int D, int rows);
 cudaError_t launch_attn_few(const moe_kv_attention_args& a, int rows, void* workspace, cudaStream_t s);
-// Requests with more than min_n tokens.
-cudaError_t launch_attn_simple(const moe_kv_attention_args& a, int min_n, cudaStream_t s);
+// Requests with more than min_n tokens; `space` 256-byte aligned.
+bool prompt_fits(int T, int G, int B);
+size_t prompt_workspace_bytes(int D);
+cudaError_t launch_attn_prompt(const moe_kv_attention_args& a, int min_n, int* status, void* space,
+                               cudaStream_t s);
 
 }  // namespace moe

@@ -1,0 +1,849 @@
+// Attention over the 8-bit paged cache for many query rows per request: prompts and chunks.
+//
+// Two matrix products of 128 x 128 x D per 128-token tile and 128 rows, so the tensor cores are the
+// bound, and the exponentials come close behind.  A block is 256 rows of one request and key/value
+// head (row = token x heads that share the head + head: any group size fills the tiles), as two tiles
+// of 128 rows that share every K and V tile, so that one tile's softmax runs while the tensor cores
+// work on the other.
+//   S = Q K^T   kind::f8f6f4: the K codes as they are; a row of Q, scaled by a power of two, as two
+//               E4M3 terms one after the other along the reduction (2 x D at twice the 16-bit rate)
+//   O += P V    kind::f16: P in FP16 from tensor memory (it takes the place of S), V codes widened to
+//               FP16, which is exact, by a warpgroup that has nothing else to do
+// The pages' scales cost nothing per value: with f = K scale x softmax scale and lv = log2 V scale a
+// probability is formed as p' = 2^(s f + lv - M), one multiply-add per value, where M is the row's
+// running maximum of s f + lv.  O = sum p' code needs no scale, the row sum is sum p' / V scale, one
+// multiply-add per 16 values.  M moves only when a row passes it by 2^8, so the rescaling of O is rare;
+// p' carries a factor of 2^4, which leaves FP16 its full precision down to 2^-18 of the maximum.
+//
+//   warp 0        producer: lane i fetches page i of a tile and its scales
+//   warp 1        MMA issuer
+//   warps 4..7    V codes -> FP16
+//   warps 8..15   softmax: thread = row, one warpgroup per tile of rows
+// Work: the blocks, longest first (k_prompt_plan), go to the CTAs in rounds, forward and back; the
+// blocks of the last, incomplete round are cut along the cache so that every SM has a piece, and
+// k_prompt_join adds the pieces in order.
+#include <algorithm>
+
+#include "kv_device.cuh"
+
+namespace moe {
+
+constexpr int kBlockRows = 256;
+constexpr int kPromptThreads = 512;
+constexpr int kPromptCtas = 152;              // at most (SMs)
+constexpr int kMaxBlocks = 1 << 16;           // blocks of a call, without the heads
+constexpr int kBins = 4096;                   // lengths that the order tells apart
+constexpr float kPromptGrow = 8.0f;           // log2 by which a row may pass its maximum
+constexpr float kPromptBias = 4.0f;           // log2 of p' at the maximum
+constexpr int kMinPieceTiles = 4;             // a piece of a cut block has at least this many tiles
+// registers of the four warpgroups, launched with 128 each
+constexpr int kRegsIssue = 56, kRegsWiden = 72, kRegsSoftmax = 192;
+static_assert(kRegsIssue + kRegsWiden + 2 * kRegsSoftmax <= 512, "register split must fit the launch");
+
+template <int kD>
+struct PromptCfg {
+  static constexpr int QTerm = 128 * kD;                 // one E4M3 term of a row tile
+  static constexpr int QBytes = 4 * QTerm;               // [row tile][term]
+  static constexpr int Half = kTile * kD;                // K or V codes of a tile
+  static constexpr int KStages = 3, VStages = 2, WStages = 2, Slots = 4;
+  static constexpr int WBytes = kTile * kD * 2;          // V of a tile in FP16
+  static constexpr int Tiles = QBytes + KStages * Half + VStages * Half + WStages * WBytes;
+  static constexpr int Smem = 1024 + Tiles + 1024 + Slots * 128;
+  static constexpr int PartFloats = kBlockRows * (kD + 2);
+  static_assert(Smem <= 232448, "shared memory");
+};
+
+// Per 16 tokens of a tile: K scale x softmax scale x log2 e, log2 V scale, 1 / V scale.
+struct PromptSlot {
+  float kf[8], lv[8], iv[8];
+  float pad[8];
+};
+
+struct PromptParams {
+  moe_kv_attention_args a;
+  int G, page_shift, min_n;
+  int2* list;                  // blocks (request, block), longest first
+  int* bins;                   // scratch of the order
+  int* count;                  // blocks
+  float* parts;                // [gridDim.x][PartFloats]
+  int* status;
+};
+
+// One block's rows and the tokens that they see; tiles [t0, t1) of it for this CTA.
+struct PromptWork {
+  int b, h, row0, rows, q0, pos0, lo, hi, t0, t1;
+  int part;                    // workspace part, -1: the whole block is here
+};
+
+__device__ __forceinline__ void prompt_block(const PromptParams& p, int b, int blk, PromptWork& w) {
+  w.b = b;
+  w.q0 = p.a.tok_start[b];
+  const int n = min(p.a.tok_start[b + 1] - w.q0, p.a.max_q);
+  const int L = min(max(p.a.kv_len[b], 0), p.a.max_pages << p.page_shift);
+  w.pos0 = L - (p.a.tok_start[b + 1] - w.q0);
+  w.row0 = blk * kBlockRows;
+  w.rows = n * p.G;
+  const int i0 = w.row0 / p.G, i1 = (min(w.rows, w.row0 + kBlockRows) - 1) / p.G;
+  w.hi = max(0, min(L, w.pos0 + i1 + 1));
+  w.lo = p.a.window > 0 ? max(0, w.pos0 + i0 - p.a.window + 1) : 0;
+  w.t0 = min(w.lo, max(w.hi - 1, 0)) / kTile;
+  w.t1 = max(w.t0 + 1, (w.hi + kTile - 1) / kTile);
+}
+
+// The k-th piece of work of this CTA; false when there is none.
+__device__ __forceinline__ bool prompt_work(const PromptParams& p, int blocks, int k, PromptWork& w) {
+  const int C = gridDim.x, c = blockIdx.x;
+  const int items = blocks * p.a.Hkv, rounds = items / C, rest = items - rounds * C;
+  int item, piece = 0, pieces = 1;
+  if (k < rounds) {
+    item = k * C + ((k & 1) ? C - 1 - c : c);
+  } else if (k == rounds && rest > 0) {
+    const int f = C / rest;
+    if (c >= rest * f) return false;
+    item = rounds * C + c / f;
+    piece = c % f;
+    pieces = f;
+  } else {
+    return false;
+  }
+  const int2 e = p.list[item / p.a.Hkv];
+  prompt_block(p, e.x, e.y, w);
+  w.h = item % p.a.Hkv;
+  w.part = -1;
+  if (pieces > 1) {
+    const int nt = w.t1 - w.t0, np = max(1, min(pieces, nt / kMinPieceTiles));
+    if (piece >= np) return false;
+    const int t0 = w.t0;
+    w.t0 = t0 + nt * piece / np;
+    w.t1 = t0 + nt * (piece + 1) / np;
+    if (np > 1) w.part = c;
+  }
+  return true;
+}
+
+// Blocks of all requests with more than min_n tokens, longest first; equal lengths keep the order of
+// requests and rows, so the order never depends on timing.
+__global__ void __launch_bounds__(1024) k_prompt_plan(const PromptParams p) {
+  __shared__ int first[kMaxRequests + 1];     // blocks before request b
+  __shared__ int hist[kBins];
+  __shared__ int sums[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  auto blocks_of = [&](int b) {
+    const int q0 = p.a.tok_start[b], n = p.a.tok_start[b + 1] - q0;
+    if (n <= p.min_n || q0 < 0 || q0 + n > p.a.T) return 0;
+    return (min(n, p.a.max_q) * p.G + kBlockRows - 1) / kBlockRows;
+  };
+  auto scan = [&](int v) {                    // inclusive sum over the block
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int t = __shfl_up_sync(~0u, v, d);
+      if (lane >= d) v += t;
+    }
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    int base = 0;
+    for (int w = 0; w < warp; ++w) base += sums[w];
+    __syncthreads();
+    return base + v;
+  };
+  const int per = (p.a.B + 1023) / 1024;
+  int mine = 0;
+  for (int b = tid * per; b < min(p.a.B, (tid + 1) * per); ++b) mine += blocks_of(b);
+  int at = scan(mine) - mine;
+  for (int b = tid * per; b < min(p.a.B, (tid + 1) * per); ++b) {
+    first[b] = at;
+    at += blocks_of(b);
+    if (b == p.a.B - 1) first[p.a.B] = at;
+  }
+  for (int i = tid; i < kBins; i += 1024) hist[i] = 0;
+  __syncthreads();
+  const int total = min(first[p.a.B], kMaxBlocks);
+  int shift = 0;                              // tiles per bin
+  while (((p.a.max_pages << p.page_shift) / kTile + 1) >> shift >= kBins) ++shift;
+  auto owner = [&](int x) {
+    int lo = 0, hi = p.a.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= x) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  };
+  for (int x = tid; x < total; x += 1024) {
+    const int b = owner(x);
+    PromptWork w;
+    prompt_block(p, b, x - first[b], w);
+    const int bin = kBins - 1 - min((w.t1 - w.t0) >> shift, kBins - 1);
+    p.bins[x] = bin;
+    atomicAdd(&hist[bin], 1);
+  }
+  __syncthreads();
+  int v[kBins / 1024], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kBins / 1024; ++i) {
+    v[i] = hist[tid * (kBins / 1024) + i];
+    sum += v[i];
+  }
+  int start = scan(sum) - sum;
+#pragma unroll
+  for (int i = 0; i < kBins / 1024; ++i) {
+    hist[tid * (kBins / 1024) + i] = start;
+    start += v[i];
+  }
+  __syncthreads();
+  if (warp == 0) {
+    for (int x0 = 0; x0 < total; x0 += 32) {
+      const int x = x0 + lane;
+      const int bin = x < total ? p.bins[x] : -1;
+      const uint32_t same = __match_any_sync(~0u, bin);
+      if (x < total) {
+        const int b = owner(x);
+        p.list[hist[bin] + __popc(same & ((1u << lane) - 1))] = make_int2(b, x - first[b]);
+      }
+      __syncwarp();
+      if (x < total && lane == __ffs(same) - 1) hist[bin] += __popc(same);
+      __syncwarp();
+    }
+    if (lane == 0) *p.count = total;
+  }
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: FP16 operands, fp32 sums, issued by one thread.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+template <int kD>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    k_attn_prompt(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const __grid_constant__ PromptParams p) {
+  using C = PromptCfg<kD>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  const uint32_t sQ = sbase, sK = sQ + C::QBytes, sV = sK + C::KStages * C::Half,
+                 sW = sV + C::VStages * C::Half;
+  uint8_t* ctrl = smem + C::Tiles;
+  PromptSlot* slots = reinterpret_cast<PromptSlot*>(ctrl + 1024);
+  const uint32_t bar0 = smem_addr(ctrl);
+  auto kfull = [&](int s) { return bar0 + 8u * s; };
+  auto kempty = [&](int s) { return bar0 + 8u * (4 + s); };
+  auto vfull = [&](int s) { return bar0 + 8u * (8 + s); };
+  auto vempty = [&](int s) { return bar0 + 8u * (12 + s); };
+  auto wfull = [&](int s) { return bar0 + 8u * (16 + s); };
+  auto wempty = [&](int s) { return bar0 + 8u * (20 + s); };
+  auto ifull = [&](int s) { return bar0 + 8u * (24 + s); };
+  auto iempty = [&](int s) { return bar0 + 8u * (28 + s); };
+  auto qfull = [&](int w) { return bar0 + 8u * (32 + w); };
+  auto sfull = [&](int w) { return bar0 + 8u * (34 + w); };
+  auto pfull = [&](int w) { return bar0 + 8u * (36 + w); };
+  auto ofull = [&](int w) { return bar0 + 8u * (38 + w); };
+  const uint32_t drain = bar0 + 8u * 40;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * 41);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* k_done = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  volatile int* v_done = reinterpret_cast<volatile int*>(tmem_slot + 3);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* status = p.status;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(kfull(s), 1);
+      mbar_init(kempty(s), 1);
+      mbar_init(vfull(s), 1);
+      mbar_init(vempty(s), 4);
+      mbar_init(wfull(s), 4);
+      mbar_init(wempty(s), 1);
+      mbar_init(ifull(s), 1);
+      mbar_init(iempty(s), 8);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(qfull(w), 4);
+      mbar_init(sfull(w), 1);
+      mbar_init(pfull(w), 4);
+      mbar_init(ofull(w), 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *k_done = 0;
+    *v_done = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  if (warp == 1) tmem_alloc(smem_addr(tmem_slot), 512);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const int blocks = *p.count;
+
+  // Tensor memory: S of row tile w (P in its first half) at 128 w, O at 256 + 128 w.
+  if (warp < 4) {
+    regs_down<kRegsIssue>();
+    if (warp == 0) {
+      // -------------------------------------------------------------------- producer
+      const int npg = kTile >> p.page_shift, P = 1 << p.page_shift;
+      bool ok = true;
+      int it = 0;
+      PromptWork w;
+      for (int k = 0; ok && prompt_work(p, blocks, k, w); ++k) {
+        auto entry = [&](int tile) {
+          const int pg = tile * npg + lane;
+          if (tile >= w.t1 || lane >= npg || (pg << p.page_shift) >= w.hi ||
+              ((pg + 1) << p.page_shift) <= w.lo)
+            return -1;
+          const int e = p.a.block_table[(size_t)w.b * p.a.max_pages + pg];
+          return e < p.a.num_pages ? e : -1;
+        };
+        auto scale = [&](const float* s, int page) {
+          return page >= 0 ? s[(size_t)page * p.a.Hkv + w.h] : 1.0f;
+        };
+        int page = entry(w.t0), page1 = entry(w.t0 + 1);
+        float ks = scale(p.a.k_scale, page), vs = scale(p.a.v_scale, page);
+        for (int t = w.t0; t < w.t1; ++t, ++it) {
+          const int page2 = entry(t + 2);
+          const float ks1 = scale(p.a.k_scale, page1), vs1 = scale(p.a.v_scale, page1);
+          const int sk = it % C::KStages, sv = it % C::VStages, si = it % C::Slots;
+          if (lane == 0)
+            ok = mbar_wait(iempty(si), ((it / C::Slots) & 1) ^ 1, abort_flag, status) &&
+                 mbar_wait(kempty(sk), ((it / C::KStages) & 1) ^ 1, abort_flag, status);
+          ok = __shfl_sync(~0u, (int)ok, 0);
+          if (!ok) break;
+          const uint32_t bytes = __popc(__ballot_sync(~0u, page >= 0)) * P * kD;
+          if (lane == 0) mbar_arrive_expect_tx(kfull(sk), bytes);
+          __syncwarp();
+          if (page >= 0)
+            tma_load_4d(sK + sk * C::Half + lane * P * kD, &tmK, 0, 0, w.h, page, kfull(sk));
+          if (lane == 0) *k_done = it + 1;      // copies issued so far
+          // scales of the tile's groups of 16 tokens
+          const int src = (lane * 16) >> p.page_shift;
+          const float gk = __shfl_sync(~0u, ks, src & 31), gv = __shfl_sync(~0u, vs, src & 31);
+          if (lane < 8) {
+            slots[si].kf[lane] = gk * p.a.sm_scale * kLog2e;
+            const float v = gv >= 0.0f ? fmaxf(gv, 1e-30f) : gv;
+            slots[si].lv[lane] = log2f(v);
+            slots[si].iv[lane] = 1.0f / v;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(ifull(si));
+            ok = mbar_wait(vempty(sv), ((it / C::VStages) & 1) ^ 1, abort_flag, status);
+          }
+          ok = __shfl_sync(~0u, (int)ok, 0);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(vfull(sv), bytes);
+          __syncwarp();
+          if (page >= 0)
+            tma_load_4d(sV + sv * C::Half + lane * P * kD, &tmV, 0, 0, w.h, page, vfull(sv));
+          if (lane == 0) *v_done = it + 1;
+          page = page1;
+          page1 = page2;
+          ks = ks1;
+          vs = vs1;
+        }
+      }
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------------------------------- MMA
+      constexpr uint32_t kIdescS = make_idesc_e4m3(128, kTile);
+      // D fp32, A and B FP16, B MN-major, 128 x kD
+      constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(kD >> 3) << 17) | (8u << 24);
+      bool ok = true;
+      int it = 0, seg = 0;                   // tiles whose P V has been issued, pieces begun
+      // S of row tile w for tile `tile`
+      auto scores = [&](int w, int tile) {
+        const uint64_t kd = rows_desc<kD>(sK + tile % C::KStages * C::Half);
+#pragma unroll
+        for (int term = 0; term < 2; ++term) {
+          const uint64_t qd = rows_desc<kD>(sQ + (2 * w + term) * C::QTerm);
+#pragma unroll
+          for (int k = 0; k < kD / 32; ++k)
+            mma_f8(tmem + 128 * w, qd + 2 * k, kd + 2 * k, kIdescS, term + k > 0);
+        }
+        mma_commit(sfull(w));
+        if (w == 1) mma_commit(kempty(tile % C::KStages));
+      };
+      auto k_ready = [&](int tile) {
+        return mbar_wait(kfull(tile % C::KStages), (tile / C::KStages) & 1, abort_flag, status);
+      };
+      auto output = [&](int w, int tile, bool first) {
+        if (!mbar_wait(pfull(w), tile & 1, abort_flag, status)) return false;
+        tc_fence_after_sync();
+        const uint32_t wt = sW + tile % C::WStages * C::WBytes;
+        // V in FP16: rows of 64 values (128 bytes), the second half of the values 16 KB further
+        uint64_t vd = make_sdesc_sw128(wt, 1024);
+        vd = (vd & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)((kTile * 128) >> 4) << 16);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_f16_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, vd + k * (16 * 128 / 16), kIdescO,
+                     !first || k > 0);
+        mma_commit(ofull(w));
+        if (w == 1) mma_commit(wempty(tile % C::WStages));
+        return true;
+      };
+      PromptWork w;
+      bool have = prompt_work(p, blocks, 0, w);
+      if (have) {
+        ok = mbar_wait(qfull(0), 0, abort_flag, status) && k_ready(0);
+        if (ok) {
+          tc_fence_after_sync();
+          scores(0, 0);
+        }
+        ok = ok && mbar_wait(qfull(1), 0, abort_flag, status);
+        if (ok) {
+          tc_fence_after_sync();
+          scores(1, 0);
+        }
+      }
+      while (ok && have) {
+        const int nt = w.t1 - w.t0;
+        for (int t = 0; ok && t < nt; ++t, ++it) {
+          if (!mbar_wait(wfull(it % C::WStages), (it / C::WStages) & 1, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          const bool more = t + 1 < nt;
+          if (!output(0, it, t == 0)) ok = false;
+          if (ok && more) {
+            ok = k_ready(it + 1);
+            if (ok) scores(0, it + 1);
+          }
+          if (ok && !output(1, it, t == 0)) ok = false;
+          if (ok && more) scores(1, it + 1);
+        }
+        ++seg;
+        have = ok && prompt_work(p, blocks, seg, w);
+        for (int r = 0; have && ok && r < 2; ++r) {
+          ok = mbar_wait(qfull(r), seg & 1, abort_flag, status) && (r == 1 || k_ready(it));
+          if (ok) {
+            tc_fence_after_sync();
+            scores(r, it);
+          }
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------------ V codes -> FP16
+    regs_down<kRegsWiden>();
+    constexpr int kChunks = kD / 16;         // 16 codes each
+    constexpr int kRowsAt = 32 / kChunks;    // rows of a warp's load
+    const int c = lane % kChunks, rl = lane / kChunks;
+    bool ok = true;
+    int it = 0;
+    PromptWork w;
+    for (int k = 0; ok && prompt_work(p, blocks, k, w); ++k) {
+      for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
+        const int sv = it % C::VStages, sw = it % C::WStages;
+        ok = mbar_wait(vfull(sv), (it / C::VStages) & 1, abort_flag, status) &&
+             mbar_wait(wempty(sw), ((it / C::WStages) & 1) ^ 1, abort_flag, status);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        const uint8_t* in = smem + (sV - sbase) + sv * C::Half;
+        uint8_t* out = smem + (sW - sbase) + sw * C::WBytes;
+        const int token0 = t * kTile;
+        const bool edge = token0 < w.lo || token0 + kTile > w.hi;
+#pragma unroll 4
+        for (int i = 0; i < 32 / kRowsAt; ++i) {
+          const int r = (warp & 3) * 32 + i * kRowsAt + rl;
+          uint4 x = *reinterpret_cast<const uint4*>(in + swz<kD>(r, 16 * c));
+          // rows that no query row sees may hold anything: 0 x NaN would spread
+          if (edge && (token0 + r < w.lo || token0 + r >= w.hi)) x = make_uint4(0, 0, 0, 0);
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+          uint32_t h[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * j]) : "h"((uint16_t)u[j]));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * j + 1]) : "h"((uint16_t)(u[j] >> 16)));
+          }
+          // lanes of the two halves store their 16-byte pieces in opposite order: no bank conflicts
+          const int half = c >> 2, col = (c & 3) * 32;
+          uint8_t* o = out + half * (kTile * 128);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int piece = e ^ half;
+            *reinterpret_cast<uint4*>(o + swz<128>(r, col + 16 * piece)) =
+                piece ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(wfull(sw));
+          mbar_arrive(vempty(sv));
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------------------- softmax
+    regs_up<kRegsSoftmax>();
+    const int wg = (warp >> 2) - 2, q = warp & 3;
+    const int tr = q * 32 + lane;            // row of the row tile
+    const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+    const uint32_t tS = tmem + lane_base + 128 * wg, tO = tmem + lane_base + 256 + 128 * wg;
+    float qs = 0.0f;                         // value of a code of the row's Q
+
+    // Q of one row: scaled so that the largest value is in [128, 256), two E4M3 terms
+    auto load_q = [&](const PromptWork& w) {
+      const int row = w.row0 + 128 * wg + tr;
+      uint4 x[kD / 8];
+      if (row < w.rows) {
+        const int i = row / p.G;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(p.a.q) + (int64_t)(w.q0 + i) * p.a.q_token_stride +
+            (int64_t)(w.h * p.G + row - i * p.G) * p.a.q_head_stride);
+#pragma unroll
+        for (int v = 0; v < kD / 8; ++v) x[v] = src[v];
+      } else {
+#pragma unroll
+        for (int v = 0; v < kD / 8; ++v) x[v] = make_uint4(0, 0, 0, 0);
+      }
+      float amax = 0.0f;
+#pragma unroll
+      for (int v = 0; v < kD / 8; ++v) {
+        const uint32_t u[4] = {x[v].x, x[v].y, x[v].z, x[v].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+      }
+      const int e = amax > 0.0f ? max((int)(__float_as_uint(amax) >> 23) - 127, -100) : 0;
+      const float mul = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+      qs = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
+      uint8_t* o = smem + wg * 2 * C::QTerm;
+#pragma unroll
+      for (int c = 0; c < kD / 16; ++c) {
+        uint32_t t1[4], t2[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 y = x[2 * c + (j >> 1)];
+          const uint32_t u0 = j & 1 ? y.z : y.x, u1 = j & 1 ? y.w : y.y;
+          const float a0 = __uint_as_float(u0 << 16) * mul, a1 = __uint_as_float(u0 & 0xFFFF0000u) * mul;
+          const float a2 = __uint_as_float(u1 << 16) * mul, a3 = __uint_as_float(u1 & 0xFFFF0000u) * mul;
+          const uint32_t c0 = cvt_e4m3x2(a0, a1), c1 = cvt_e4m3x2(a2, a3);
+          float f0, f1, f2, f3;
+          e4m3x2_to_f32(c0, f0, f1);
+          e4m3x2_to_f32(c1, f2, f3);
+          t1[j] = c0 | (c1 << 16);
+          t2[j] = cvt_e4m3x2(a0 - f0, a1 - f1) | (cvt_e4m3x2(a2 - f2, a3 - f3) << 16);
+        }
+        *reinterpret_cast<uint4*>(o + swz<kD>(tr, 16 * c)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+        *reinterpret_cast<uint4*>(o + C::QTerm + swz<kD>(tr, 16 * c)) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qfull(wg));
+    };
+
+    bool ok = true;
+    int it = 0;
+    PromptWork w, nw;
+    bool have = prompt_work(p, blocks, 0, w);
+    if (have) load_q(w);
+    for (int k = 0; ok && have; ++k) {
+      // tokens that this row sees, and those that every / any row of the tile sees
+      const int row = w.row0 + 128 * wg + tr;
+      const bool live = row < w.rows;
+      const int pos = w.pos0 + row / p.G;
+      const int see_lo = p.a.window > 0 ? max(0, pos - p.a.window + 1) : 0, see_hi = live ? pos + 1 : 0;
+      const int r_first = w.row0 + 128 * wg, r_last = min(w.rows, r_first + 128) - 1;
+      const int all_hi = w.pos0 + r_first / p.G + 1;
+      const int all_lo = p.a.window > 0 ? w.pos0 + r_last / p.G - p.a.window + 1 : 0;
+      float M = -INFINITY, l = 0.0f;
+      bool more = false;
+      for (int t = w.t0; t < w.t1; ++t, ++it) {
+        const int si = it % C::Slots;
+        ok = mbar_wait(ifull(si), (it / C::Slots) & 1, abort_flag, status) &&
+             mbar_wait(sfull(wg), it & 1, abort_flag, status);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const PromptSlot& slot = slots[si];
+        const int token0 = t * kTile;
+        const bool edge = token0 + kTile > all_hi || token0 < all_lo;
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+        tmem_ld_wait();
+        float* x = reinterpret_cast<float*>(s);
+        if (edge) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const float f = slot.kf[g] * qs, lv = slot.lv[g];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int j = token0 + 16 * g + i;
+              x[16 * g + i] = j >= see_lo && j < see_hi ? __fmaf_rn(x[16 * g + i], f, lv) : -INFINITY;
+            }
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          float m = x[16 * g];
+#pragma unroll
+          for (int i = 1; i < 16; ++i) m = fmaxf(m, x[16 * g + i]);
+          top = fmaxf(top, edge ? m : __fmaf_rn(m, slot.kf[g] * qs, slot.lv[g]));
+        }
+        if (__any_sync(~0u, top > M + kPromptGrow)) {
+          const float mn = fmaxf(M, top);
+          const float alpha = M == mn ? 1.0f : exp2_approx(M - mn);
+          if (t > w.t0) {
+            // O so far is relative to the old maximum
+            ok = mbar_wait(ofull(wg), (it - 1) & 1, abort_flag, status);
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            tc_fence_after_sync();
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(tO + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(tO + c, o);
+            }
+            tmem_st_wait();
+          }
+          l *= alpha;
+          M = mn;
+        }
+        const float base = kPromptBias - (M == -INFINITY ? 0.0f : M);
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const float f = edge ? 1.0f : slot.kf[g] * qs;
+          const float add = edge ? base : slot.lv[g] + base;
+          float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float p0 = exp2_approx(__fmaf_rn(x[16 * g + i], f, add));
+            const float p1 = exp2_approx(__fmaf_rn(x[16 * g + i + 1], f, add));
+            sum0 += p0;
+            sum1 += p1;
+            s[8 * g + i / 2] = pack_f16x2(p0, p1);
+          }
+          l = __fmaf_rn(sum0 + sum1, slot.iv[g], l);
+        }
+        tmem_st32(tS, s);
+        tmem_st32(tS + 32, s + 32);
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(iempty(si));
+          mbar_arrive(pfull(wg));
+        }
+      }
+      if (!ok) break;
+      // the next piece's Q goes in while the last P V runs
+      more = prompt_work(p, blocks, k + 1, nw);
+      if (more) load_q(nw);
+      ok = mbar_wait(ofull(wg), (it - 1) & 1, abort_flag, status);
+      ok = __all_sync(~0u, ok);
+      if (!ok) break;
+      tc_fence_after_sync();
+      if (w.part >= 0) {
+        float* o = p.parts + (size_t)w.part * C::PartFloats + 128 * wg + tr;
+#pragma unroll 1
+        for (int c = 0; c < kD; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(tO + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[(c + i) * kBlockRows] = __uint_as_float(v[i]);
+        }
+        o[kD * kBlockRows] = M;
+        o[(kD + 1) * kBlockRows] = l;
+      } else {
+        const int i = row / p.G;
+        uint16_t* o = static_cast<uint16_t*>(p.a.out) + (int64_t)(w.q0 + i) * p.a.out_token_stride +
+                      (int64_t)(w.h * p.G + row - i * p.G) * p.a.out_head_stride;
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < kD; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(tO + c, v);
+          tmem_ld_wait();
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t r[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                const float a = __uint_as_float(v[8 * j + 2 * h]), b = __uint_as_float(v[8 * j + 2 * h + 1]);
+                // a row that saw nothing may have met anything in O
+                r[h] = inv != 0.0f ? pack_bf16x2(a * inv, b * inv) : 0u;
+              }
+              *reinterpret_cast<uint4*>(o + c + 8 * j) = make_uint4(r[0], r[1], r[2], r[3]);
+            }
+          }
+        }
+      }
+      tc_fence_before_sync();
+      w = nw;
+      have = more;
+    }
+  }
+
+  // ------------------------------------------------------------------------ teardown
+  __syncthreads();
+  auto drain_wait = [&](uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        atomicCAS(status, 0, (int)MOE_ERR_DEVICE_TIMEOUT);
+        return;
+      }
+    }
+  };
+  if (warp == 1 && lane == 0) {
+    mma_commit(drain);
+    drain_wait(drain, 0);
+  }
+  if (warp == 0 && lane == 0 && *abort_flag) {
+    // copies still in flight: the latest use of each stage
+    for (int i = max(0, *k_done - C::KStages); i < *k_done; ++i)
+      drain_wait(kfull(i % C::KStages), (i / C::KStages) & 1);
+    for (int i = max(0, *v_done - C::VStages); i < *v_done; ++i)
+      drain_wait(vfull(i % C::VStages), (i / C::VStages) & 1);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Adds the pieces of the blocks that the last round cut.  blockIdx.x: block of that round, blockIdx.y:
+// 16 values; thread = row.
+template <int kD>
+__global__ void __launch_bounds__(kBlockRows) k_prompt_join(const PromptParams p, int ctas) {
+  using C = PromptCfg<kD>;
+  grid_dep_wait();
+  const int items = *p.count * p.a.Hkv, rounds = items / ctas, rest = items - rounds * ctas;
+  const int x = blockIdx.x;
+  if (x >= rest) return;
+  const int item = rounds * ctas + x, f = ctas / rest;
+  const int2 e = p.list[item / p.a.Hkv];
+  PromptWork w;
+  prompt_block(p, e.x, e.y, w);
+  const int np = max(1, min(f, (w.t1 - w.t0) / kMinPieceTiles));
+  if (np == 1) return;
+  const int h = item % p.a.Hkv, row = w.row0 + threadIdx.x;
+  if (row >= w.rows) return;
+  const float* parts = p.parts + (size_t)(x * f) * C::PartFloats + threadIdx.x;
+  float M = -INFINITY;
+  for (int i = 0; i < np; ++i) M = fmaxf(M, parts[(size_t)i * C::PartFloats + kD * kBlockRows]);
+  float l = 0.0f, acc[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
+  const int c0 = blockIdx.y * 16;
+  for (int i = 0; i < np; ++i) {
+    const float* o = parts + (size_t)i * C::PartFloats;
+    const float m = o[kD * kBlockRows];
+    // a piece whose tokens this row does not see has an empty sum
+    if (m == -INFINITY) continue;
+    const float wgt = m == M ? 1.0f : exp2_approx(m - M);
+    l = __fmaf_rn(o[(kD + 1) * kBlockRows], wgt, l);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j] = __fmaf_rn(o[(c0 + j) * kBlockRows], wgt, acc[j]);
+  }
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  const int i = row / p.G;
+  uint16_t* out = static_cast<uint16_t*>(p.a.out) + (int64_t)(w.q0 + i) * p.a.out_token_stride +
+                  (int64_t)(h * p.G + row - i * p.G) * p.a.out_head_stride + c0;
+#pragma unroll
+  for (int j = 0; j < 16; j += 8) {
+    uint4 r;
+    r.x = pack_bf16x2(acc[j] * inv, acc[j + 1] * inv);
+    r.y = pack_bf16x2(acc[j + 2] * inv, acc[j + 3] * inv);
+    r.z = pack_bf16x2(acc[j + 4] * inv, acc[j + 5] * inv);
+    r.w = pack_bf16x2(acc[j + 6] * inv, acc[j + 7] * inv);
+    *reinterpret_cast<uint4*>(out + j) = r;
+  }
+}
+
+// ------------------------------------------------------------------------------------ launch
+bool prompt_fits(int T, int G, int B) {
+  return (long long)T * G / kBlockRows + B <= kMaxBlocks;
+}
+
+size_t prompt_workspace_bytes(int D) {
+  return 256 + kMaxBlocks * sizeof(int2) + kMaxBlocks * sizeof(int) +
+         (size_t)kPromptCtas * kBlockRows * (D + 2) * 4;
+}
+
+template <int kD>
+static cudaError_t launch_prompt(const moe_kv_attention_args& a, int min_n, int* status, void* space,
+                                 cudaStream_t s) {
+  using C = PromptCfg<kD>;
+  CUtensorMap tmK, tmV;
+  if (!cache_map(&tmK, a.k_codes, kD, a.page_size, a.Hkv, a.num_pages) ||
+      !cache_map(&tmV, a.v_codes, kD, a.page_size, a.Hkv, a.num_pages))
+    return cudaErrorInvalidValue;
+  cudaError_t err = cudaFuncSetAttribute(k_attn_prompt<kD>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem);
+  if (err != cudaSuccess) return err;
+  PromptParams p;
+  p.a = a;
+  p.G = a.Hq / a.Hkv;
+  p.page_shift = __builtin_ctz((unsigned)a.page_size);
+  p.min_n = min_n;
+  uint8_t* ws = static_cast<uint8_t*>(space);
+  p.count = reinterpret_cast<int*>(ws);
+  p.list = reinterpret_cast<int2*>(ws + 256);
+  p.bins = reinterpret_cast<int*>(ws + 256 + kMaxBlocks * sizeof(int2));
+  p.parts = reinterpret_cast<float*>(ws + 256 + kMaxBlocks * (sizeof(int2) + sizeof(int)));
+  p.status = status;
+  const int ctas = std::min(kPromptCtas, sm_count());
+  err = launch_pdl(k_prompt_plan, dim3(1), dim3(1024), 0, s, p);
+  if (err != cudaSuccess) return err;
+  err = launch_pdl(k_attn_prompt<kD>, dim3(ctas), dim3(kPromptThreads), C::Smem, s, tmK, tmV, p);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(k_prompt_join<kD>, dim3(ctas, kD / 16), dim3(kBlockRows), 0, s, p, ctas);
+}
+
+cudaError_t launch_attn_prompt(const moe_kv_attention_args& a, int min_n, int* status, void* space,
+                               cudaStream_t s) {
+  return a.D == 128 ? launch_prompt<128>(a, min_n, status, space, s)
+                    : launch_prompt<64>(a, min_n, status, space, s);
+}
+
+}  // namespace moe
