@@ -13,10 +13,11 @@
 // three (x 1, x 32, x 1024: 12 bits down to 2^-13 of the running maximum, 8 at 2^-17, 4 at 2^-21).
 // The page's K scale multiplies the score, its V scale the probability, relative to the tile's largest.
 //
-// The units of work, 128-token tiles of (request, head), are dealt out evenly: CTA c takes units
-// [c U / G, (c + 1) U / G) of the flattened list, whatever the lengths (G = CTAs, at most U).  A CTA that holds part of an
-// item leaves its sums, maximum and unscaled output in the workspace, and k_attn_join adds the parts
-// in CTA order, so results do not depend on timing.
+// The work is dealt out evenly, whatever the lengths: an item (request, head) weighs kItemUnits, what
+// its start and end cost, and one unit per 128-token tile; CTA c takes the tiles that lie in
+// [c U / G, (c + 1) U / G) of the flattened list (G = CTAs, at most U).  A CTA that holds part of an item
+// leaves its sums, maximum and unscaled output in the workspace, and k_attn_join adds the parts in CTA
+// order, so results do not depend on timing.
 //   warp 0      producer: lane i fetches page i of the tile (TMA), its scales and the tile's bounds
 //   warp 1      MMA issuer
 //   warps 2..   one warpgroup per 16 rows: thread = token for the scores, = d for the output
@@ -30,6 +31,7 @@ namespace moe {
 
 constexpr float kPScale = 32.0f;           // P = 1 at the running maximum becomes 32 (up to 256)
 constexpr float kGrow = 3.0f;              // log2 by which a score may pass the maximum
+constexpr int kItemUnits = 3;              // start and end of an item, in tiles
 constexpr float kTermStep = 32.0f;         // each further E4M3 term is scaled up by this
 
 template <int kD, int kNR>
@@ -60,7 +62,7 @@ struct FewSlot {
   int token0;                  // first token of the tile
   int lo, hi;                  // tokens that some row sees
   int pos0, rows, q0, head;    // position of query token 0, live rows, row of it in q, key/value head
-  int flags;                   // 2: last tile of the segment (of this CTA's part of the item)
+  int flags;                   // 2: last tile of the segment (the CTA's part of the item), 4: of the CTA
   int part;                    // workspace part that the segment fills, -1: the whole item is here
   int pad[6];
 };
@@ -98,15 +100,15 @@ __device__ __forceinline__ FewItem few_item(const FewParams& p, int b) {
   return it;
 }
 
-// Position in the CTA's units.
+// Position in the CTA's tiles.
 template <int kNR>
 struct FewWalk {
   int b, h, tile;
   FewItem item;
-  long long left;              // units from here to the CTA's end
+  long long left;              // units from this tile to the CTA's end; <= 0: no tile here
   __device__ __forceinline__ void next(const FewParams& p) {
-    if (--left <= 0) return;
-    if (++tile < item.tiles) return;
+    if (--left <= 0 || ++tile < item.tiles) return;
+    if ((left -= kItemUnits) <= 0) return;
     tile = 0;
     if (++h < p.a.Hkv) return;
     h = 0;
@@ -202,12 +204,13 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
   if (warp == 1) tmem_alloc(smem_addr(tmem_slot), C::TmemCols);
 
   // ------------------------------------------------------------ the CTA's share of the units
-  // units of request b: Hkv x tiles; an exclusive sum over threads with consecutive requests each
+  // an exclusive sum over threads with consecutive requests each
+  auto weight = [&](const FewItem& it) { return it.tiles ? (long long)(it.tiles + kItemUnits) * p.a.Hkv : 0ll; };
   grid_dep_wait();
   const int per = (p.a.B + C::Threads - 1) / C::Threads;
   const int rb0 = threadIdx.x * per, rb1 = min(p.a.B, rb0 + per);
   long long mine = 0;
-  for (int b = rb0; b < rb1; ++b) mine += (long long)few_item<kNR>(p, b).tiles * p.a.Hkv;
+  for (int b = rb0; b < rb1; ++b) mine += weight(few_item<kNR>(p, b));
   long long pre = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -234,8 +237,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
   if (u0 < u1 && u0 >= pre && u0 < pre + mine) {
     long long at = pre;
     for (int b = rb0; b < rb1; ++b) {
-      const FewItem it = few_item<kNR>(p, b);
-      const long long w = (long long)it.tiles * p.a.Hkv;
+      const long long w = weight(few_item<kNR>(p, b));
       if (u0 < at + w) {
         scan[kWarps] = b;
         scan[kWarps + 1] = u0 - at;
@@ -245,20 +247,25 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
     }
   }
   __syncthreads();
-  const int units = (int)(u1 - u0);
-  const int first_b = (int)scan[kWarps];
-  const int first_u = (int)scan[kWarps + 1];
+  // the first tile of the share: where the share begins within an item's own units, tile 0 follows
+  FewWalk<kNR> cur;
+  cur.left = u1 - u0;
+  cur.b = cur.h = cur.tile = 0;
+  cur.item = FewItem{};
+  if (u0 < u1) {
+    cur.b = (int)scan[kWarps];
+    cur.item = few_item<kNR>(p, cur.b);
+    const int u = (int)scan[kWarps + 1], per_item = cur.item.tiles + kItemUnits;
+    cur.h = u / per_item;
+    const int at = u - cur.h * per_item - kItemUnits;
+    cur.tile = max(at, 0);
+    cur.left += min(at, 0);
+  }
 
   int issued = 0;
-  if (units > 0) {
+  if (cur.left > 0) {
     if (warp == 0) {
       // -------------------------------------------------------------------- producer
-      FewWalk<kNR> cur;
-      cur.b = first_b;
-      cur.item = few_item<kNR>(p, first_b);
-      cur.h = first_u / cur.item.tiles;
-      cur.tile = first_u - cur.h * cur.item.tiles;
-      cur.left = units;
       const int npg = kTile >> p.page_shift, P = 1 << p.page_shift;
       // lane i: entry of page i of the tile; -1 where the tile needs none
       auto entry = [&](const FewWalk<kNR>& w) {
@@ -285,7 +292,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       scales(cur, page, ks, vs);
       int head_item = -1, tail_item = -1, tail_part = -1, seg = 0;
       bool first = true;
-      for (int it = 0; it < units; ++it) {
+      for (int it = 0; cur.left > 0; ++it) {
         const int page2 = entry(far);
         float ks1, vs1;
         scales(nxt, page1, ks1, vs1);
@@ -315,7 +322,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         }
         if (lane == 0) {
           const bool begin = cur.tile == 0, end = cur.tile == cur.item.tiles - 1;
-          const bool last = cur.left == 1;
+          const bool last = nxt.left <= 0;
           const int item = cur.b * p.a.Hkv + cur.h;
           slot.vref = vref;
           slot.token0 = (cur.item.tile0 + cur.tile) * kTile;
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           slot.rows = cur.item.n * p.G;
           slot.q0 = cur.item.q0;
           slot.head = cur.h;
-          slot.flags = end || last ? 2 : 0;
+          slot.flags = (end || last ? 2 : 0) | (last ? 4 : 0);
           if (first && !begin) head_item = item;
           // the segment's part of the workspace; an item that lies wholly in this CTA needs none
           const int part = 2 * (int)blockIdx.x + (seg > 0 ? 1 : 0);
@@ -355,7 +362,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         constexpr uint32_t kIdescO = make_idesc_e4m3(kD, 3 * kNR) | (1u << 15);   // A = V^T: MN-major
         const uint64_t qd = rows_desc<kD>(sQ), pd = rows_desc<128>(sP);
         int segs = 0;
-        bool ok = true;
+        const bool ok = true;
         auto scores = [&](int it) {
           const int s = it % C::Stages;
           if (!mbar_wait(kfull(s), (it / C::Stages) & 1, abort_flag, status)) return false;
@@ -367,17 +374,16 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           mma_commit(sfull(it & 1));
           return true;
         };
-        for (int it = 0; ok && it < units; ++it) {
+        for (int it = 0; ok; ++it) {
           const int s = it % C::Stages;
-          // the slot of tile it + 1 may not be there yet; only its segment flag is needed
           if (it == 0) {
             if (!mbar_wait(qfull, segs & 1, abort_flag, status) || !scores(0)) break;
             ++segs;
           }
           if (!mbar_wait(ifull(s), (it / C::Stages) & 1, abort_flag, status)) break;
           const int flags = *reinterpret_cast<volatile int*>(&slots[s].flags);
-          const bool more = it + 1 < units, same = !(flags & 2);
-          if (more && same && !scores(it + 1)) break;
+          const bool more = !(flags & 4), same = !(flags & 2);
+          if (same && !scores(it + 1)) break;
           if (!mbar_wait(pfull, it & 1, abort_flag, status) ||
               !mbar_wait(vfull(s), (it / C::Stages) & 1, abort_flag, status))
             break;
@@ -393,6 +399,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
             if (!mbar_wait(qfull, segs & 1, abort_flag, status) || !scores(it + 1)) break;
             ++segs;
           }
+          if (!more) break;
         }
       }
     } else {
@@ -429,66 +436,73 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         }
         tc_fence_before_sync();
       };
-      for (int it = 0; it < units; ++it) {
+      // Q of the segment that begins with tile `it`: 8 threads a row, D / 8 values each, two E4M3 terms.
+      // The scores of the segment before are done: this warpgroup has read them.
+      auto load_q = [&](int it) {
+        const int s = it % C::Stages;
+        if (!mbar_wait(ifull(s), (it / C::Stages) & 1, abort_flag, status)) bad = true;
+        const int rows = bad ? 0 : slots[s].rows, q0 = slots[s].q0, head = slots[s].head;
+        constexpr int kV = kD / 8;
+        const int r = r0 + (wt >> 3), c = wt & 7;
+        float x[kV];
+#pragma unroll
+        for (int i = 0; i < kV; ++i) x[i] = 0.0f;
+        if (r < rows) {
+          const int i = r / p.G;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              static_cast<const uint16_t*>(p.a.q) + (int64_t)(q0 + i) * p.a.q_token_stride +
+              (int64_t)(head * p.G + r - i * p.G) * p.a.q_head_stride + c * kV);
+#pragma unroll
+          for (int v = 0; v < kV / 8; ++v) {
+            const uint4 w = src[v];
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              x[8 * v + 2 * j] = __uint_as_float(u[j] << 16);
+              x[8 * v + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+            }
+          }
+        }
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) amax = fmaxf(amax, fabsf(x[i]));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+        // amax x mul in [128, 256)
+        const int e = amax > 0.0f ? max((int)(__float_as_uint(amax) >> 23) - 127, -100) : 0;
+        const float mul = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+        uint32_t t1[kV / 4], t2[kV / 4];
+#pragma unroll
+        for (int i = 0; i < kV / 4; ++i) {
+          t1[i] = t2[i] = 0;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float a = x[4 * i + 2 * j] * mul, b = x[4 * i + 2 * j + 1] * mul;
+            const uint32_t code = cvt_e4m3x2(a, b);
+            float fa, fb;
+            e4m3x2_to_f32(code, fa, fb);
+            t1[i] |= code << (16 * j);
+            t2[i] |= cvt_e4m3x2((a - fa) * kTermStep, (b - fb) * kTermStep) << (16 * j);
+          }
+        }
+        uint8_t* qb = smem + C::Stages * C::StageBytes;
+#pragma unroll
+        for (int i = 0; i < kV / 4; i += 2) {
+          *reinterpret_cast<uint2*>(qb + swz<kD>(r, c * kV + 4 * i)) = make_uint2(t1[i], t1[i + 1]);
+          *reinterpret_cast<uint2*>(qb + swz<kD>(kNR + r, c * kV + 4 * i)) = make_uint2(t2[i], t2[i + 1]);
+        }
+        if (c == 0) wqs[wt >> 3] = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
+        fence_proxy_async_smem();
+        named_barrier_sync(1 + wg, 128);
+        if (lane == 0) mbar_arrive(qfull);
+      };
+      load_q(0);
+      for (int it = 0;; ++it) {
         const int s = it % C::Stages;
         if (!mbar_wait(ifull(s), (it / C::Stages) & 1, abort_flag, status)) bad = true;
         const FewSlot& slot = slots[s];
         const int rows = bad ? 0 : slot.rows, pos0 = slot.pos0, q0 = slot.q0, head = slot.head;
         if (begin) {
-          // the segment's rows of Q: 8 threads a row, D / 8 values each, two E4M3 terms
-          constexpr int kV = kD / 8;
-          const int r = r0 + (wt >> 3), c = wt & 7;
-          float x[kV];
-#pragma unroll
-          for (int i = 0; i < kV; ++i) x[i] = 0.0f;
-          if (r < rows) {
-            const int i = r / p.G;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                static_cast<const uint16_t*>(p.a.q) + (int64_t)(q0 + i) * p.a.q_token_stride +
-                (int64_t)(head * p.G + r - i * p.G) * p.a.q_head_stride + c * kV);
-#pragma unroll
-            for (int v = 0; v < kV / 8; ++v) {
-              const uint4 w = src[v];
-              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                x[8 * v + 2 * j] = __uint_as_float(u[j] << 16);
-                x[8 * v + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-              }
-            }
-          }
-          float amax = 0.0f;
-#pragma unroll
-          for (int i = 0; i < kV; ++i) amax = fmaxf(amax, fabsf(x[i]));
-#pragma unroll
-          for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-          // amax x mul in [128, 256)
-          const int e = amax > 0.0f ? max((int)(__float_as_uint(amax) >> 23) - 127, -100) : 0;
-          const float mul = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-          uint32_t t1[kV / 4], t2[kV / 4];
-#pragma unroll
-          for (int i = 0; i < kV / 4; ++i) {
-            t1[i] = t2[i] = 0;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float a = x[4 * i + 2 * j] * mul, b = x[4 * i + 2 * j + 1] * mul;
-              const uint32_t code = cvt_e4m3x2(a, b);
-              float fa, fb;
-              e4m3x2_to_f32(code, fa, fb);
-              t1[i] |= code << (16 * j);
-              t2[i] |= cvt_e4m3x2((a - fa) * kTermStep, (b - fb) * kTermStep) << (16 * j);
-            }
-          }
-          uint8_t* qb = smem + C::Stages * C::StageBytes;
-#pragma unroll
-          for (int i = 0; i < kV / 4; i += 2) {
-            *reinterpret_cast<uint2*>(qb + swz<kD>(r, c * kV + 4 * i)) = make_uint2(t1[i], t1[i + 1]);
-            *reinterpret_cast<uint2*>(qb + swz<kD>(kNR + r, c * kV + 4 * i)) = make_uint2(t2[i], t2[i + 1]);
-          }
-          if (c == 0) wqs[wt >> 3] = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
-          fence_proxy_async_smem();
-          named_barrier_sync(1 + wg, 128);
-          if (lane == 0) mbar_arrive(qfull);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             m[i] = -INFINITY;
@@ -587,12 +601,14 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         vref_prev = slot.vref;
         pending = true;
         const int part = slot.part;
-        begin = slot.flags & 2;
+        const int flags = slot.flags;
+        begin = flags & 2;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(pfull);
         if (begin) {
           // ------------------------------------------------------- end of the segment
+          if (!(flags & 4)) load_q(it + 1);    // while the last P V runs
           add_output(it);
           pending = false;
           const float sum = warp_reduce16<false>(l, lane);
@@ -618,6 +634,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
             }
           }
           named_barrier_sync(1 + wg, 128);     // the sums have been read
+          if (flags & 4) break;
         }
       }
     }
@@ -657,44 +674,73 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
 
 // Joins the parts of an item that several CTAs hold.  Block c looks after the item that CTA c leaves
 // open (if any): CTA c's last segment, then the first segments of the CTAs that continue it.
-// blockIdx.y: rows, 4 a block (8 at D = 64).
+// blockIdx.y: rows, one after another.  The parts' weights are formed by all threads at once and the
+// outputs added with several loads under way, since latency is all there is to it.
 template <int kD, int kNR>
-__global__ void __launch_bounds__(128) k_attn_join(const FewParams p, int ctas) {
+__global__ void __launch_bounds__(kD) k_attn_join(const FewParams p, int ctas) {
+  __shared__ float wgt[304], red[kD / 32], red2[kD / 32];
   grid_dep_wait();
-  const int c = blockIdx.x;
+  const int c = blockIdx.x, tid = threadIdx.x;
   const int4 me = p.meta[c];
   if (me.y < 0) return;
   const int b = me.y / p.a.Hkv, h = me.y - b * p.a.Hkv;
   const int q0 = p.a.tok_start[b], rows = (p.a.tok_start[b + 1] - q0) * p.G;
-  constexpr int kRows = 512 / kD;
-  const int row0 = blockIdx.y * kRows;
-  if (row0 >= rows) return;
   // parts: this CTA's last segment, then those of CTAs c + 1 .. c + n - 1
   int n = 1;
-  for (int base = c + 1; base < ctas; base += 128) {
-    const int at = base + threadIdx.x;
+  for (int base = c + 1; base < ctas; base += kD) {
+    const int at = base + tid;
     const int got = __syncthreads_count(at < ctas && p.meta[at].x == me.y);
     n += got;
-    if (got < 128) break;
+    if (got < kD) break;
   }
   constexpr size_t kPart = kNR * (kD + 2);
-  auto part = [&](int i) { return p.parts + (size_t)(i == 0 ? me.z : 2 * (c + i)) * kPart; };
-  const int d = threadIdx.x & (kD - 1);
-  for (int row = row0 + threadIdx.x / kD; row < min(rows, row0 + kRows); row += 128 / kD) {
-    float m = -INFINITY;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, part(i)[kNR * kD + 2 * row]);
-    float l = 0.0f, acc = 0.0f;
-    for (int i = 0; i < n; ++i) {
-      const float* o = part(i);
-      const float mi = o[kNR * kD + 2 * row];
-      const float w = mi == m ? 1.0f : exp2_approx(mi - m);
-      l = __fmaf_rn(o[kNR * kD + 2 * row + 1], w, l);
-      acc = __fmaf_rn(o[row * kD + d], w, acc);
+  const float* part0 = p.parts + (size_t)me.z * kPart;
+  const float* rest = p.parts + (size_t)(2 * c) * kPart;     // part i >= 1 is 2 (c + i)
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+    constexpr int kMine = (304 + kD - 1) / kD;
+    float mi[kMine], li[kMine], m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int i = tid + k * kD;
+      mi[k] = -INFINITY;
+      li[k] = 0.0f;
+      if (i < n) {
+        const float* o = (i == 0 ? part0 : rest + 2 * i * kPart) + kNR * kD + 2 * row;
+        mi[k] = o[0];
+        li[k] = o[1];
+      }
+      m = fmaxf(m, mi[k]);
     }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    if ((tid & 31) == 0) red[tid >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kD / 32; ++w) m = fmaxf(m, red[w]);
+    float l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int i = tid + k * kD;
+      const float w = mi[k] == m ? 1.0f : exp2_approx(mi[k] - m);
+      if (i < n) wgt[i] = w;
+      l = __fmaf_rn(li[k], w, l);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+    if ((tid & 31) == 0) red2[tid >> 5] = l;
+    __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kD / 32; ++w) l += red2[w];
+    float acc = part0[row * kD + tid] * wgt[0];
+    const float* o = rest + row * kD + tid;
+#pragma unroll 8
+    for (int i = 1; i < n; ++i) acc = __fmaf_rn(o[2 * i * kPart], wgt[i], acc);
     const int i = row / p.G;
     static_cast<uint16_t*>(p.a.out)[(int64_t)(q0 + i) * p.a.out_token_stride +
-                                    (int64_t)(h * p.G + row - i * p.G) * p.a.out_head_stride + d] =
+                                    (int64_t)(h * p.G + row - i * p.G) * p.a.out_head_stride + tid] =
         (uint16_t)f32_to_bf16_bits(l > 0.0f || l != l ? acc / l : 0.0f);
+    __syncthreads();
   }
 }
 
@@ -735,7 +781,7 @@ static cudaError_t launch(const moe_kv_attention_args& a, void* workspace, cudaS
   err = launch_pdl(k_attn_few<kD, kNR>, dim3(ctas), dim3(C::Threads), C::Smem, s, tmK, tmV, p);
   if (err != cudaSuccess) return err;
   const int rows = std::min<long long>((long long)p.G * a.max_q, kNR);
-  return launch_pdl(k_attn_join<kD, kNR>, dim3(ctas, (rows + 512 / kD - 1) / (512 / kD)), dim3(128), 0, s, p, ctas);
+  return launch_pdl(k_attn_join<kD, kNR>, dim3(ctas, std::min(rows, 8)), dim3(kD), 0, s, p, ctas);
 }
 
 cudaError_t launch_attn_few(const moe_kv_attention_args& a, int nr, void* workspace, cudaStream_t s) {
