@@ -1,6 +1,8 @@
 // Host side of the paged cache's C ABI: argument checks, then one launch each.
 #include <math.h>
 
+#include <algorithm>
+
 #include "kv_internal.h"
 
 namespace moe {
@@ -124,13 +126,15 @@ moe_status moe_kv_attention(const moe_kv_attention_args* a, void* workspace, siz
       !stride_ok(a->out_head_stride))
     return MOE_ERR_INVALID_ARG;
   if (a->num_pages == 0) return MOE_ERR_INVALID_ARG;
+  moe_kv_attention_args c = *a;
+  c.window = std::min(a->window, 1 << 30);               // positions + window stay within 32 bits
   const int G = a->Hq / a->Hkv, rows = few_rows(G, a->max_q);
   const bool prompts = (long long)G * a->max_q > rows;   // some request may have more rows than that
   if (prompts && !prompt_fits(a->T, G, a->B)) return MOE_ERR_UNSUPPORTED_SHAPE;
-  cudaError_t err = launch_attn_few(*a, rows, workspace, (cudaStream_t)stream);
+  cudaError_t err = launch_attn_few(c, rows, workspace, (cudaStream_t)stream);
   if (err == cudaSuccess && prompts) {
     const size_t few = (few_workspace_bytes(a->D, rows) + 255) & ~(size_t)255;
-    err = launch_attn_prompt(*a, rows / G, static_cast<int*>(workspace),
+    err = launch_attn_prompt(c, rows / G, static_cast<int*>(workspace),
                              static_cast<uint8_t*>(workspace) + few, (cudaStream_t)stream);
   }
   return launched(err);

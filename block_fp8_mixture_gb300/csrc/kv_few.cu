@@ -33,6 +33,8 @@ constexpr float kPScale = 32.0f;           // P = 1 at the running maximum becom
 constexpr float kGrow = 3.0f;              // log2 by which a score may pass the maximum
 constexpr int kItemUnits = 3;              // start and end of an item, in tiles
 constexpr float kTermStep = 32.0f;         // each further E4M3 term is scaled up by this
+constexpr float kNoScore = -3e38f;         // running maximum before the first token: finite, so that
+                                           // a masked score (-inf) minus it stays -inf
 
 template <int kD, int kNR>
 struct FewCfg {
@@ -147,8 +149,29 @@ __device__ __forceinline__ float warp_reduce16(float (&v)[16], int lane) {
   return kMax ? fmaxf(v[0], got) : v[0] + got;
 }
 
-__device__ __forceinline__ void st_u8(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+// Two FP16 values -> the E4M3 codes nearest to them, and 32 x what those leave over (exact in FP16:
+// the difference has fewer bits than the value).
+__device__ __forceinline__ uint32_t take_term(uint32_t& h2) {
+  uint16_t code;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(code) : "r"(h2));
+  uint32_t back;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(code));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h2) : "r"(back));
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h2) : "r"(0x50005000u));
+  return code;
+}
+
+// P lies token by token (MN-major B): 8 tokens x 16 rows of one term are 128 contiguous bytes, the
+// terms' and warpgroups' 16-row pieces follow each other, then the next 8 tokens.
+template <int kNR>
+__device__ __forceinline__ uint64_t p_desc(uint32_t saddr) {
+  constexpr uint32_t kPieces = 3 * kNR / 16;
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFF) >> 4);
+  d |= (uint64_t)((kPieces * 128) >> 4) << 16;   // between groups of 8 tokens
+  d |= (uint64_t)(128 >> 4) << 32;               // between pieces of 16 rows
+  d |= (uint64_t)1 << 46;
+  return d;
 }
 
 template <int kD, int kNR>
@@ -359,8 +382,8 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       // ------------------------------------------------------------------------- MMA
       if (lane == 0) {
         constexpr uint32_t kIdescS = make_idesc_e4m3(kTile, 2 * kNR);
-        constexpr uint32_t kIdescO = make_idesc_e4m3(kD, 3 * kNR) | (1u << 15);   // A = V^T: MN-major
-        const uint64_t qd = rows_desc<kD>(sQ), pd = rows_desc<128>(sP);
+        constexpr uint32_t kIdescO = make_idesc_e4m3(kD, 3 * kNR) | (3u << 15);   // both MN-major
+        const uint64_t qd = rows_desc<kD>(sQ), pd = p_desc<kNR>(sP);
         int segs = 0;
         const bool ok = true;
         auto scores = [&](int it) {
@@ -391,7 +414,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           const uint32_t sv = sbase + s * C::StageBytes + C::HalfBytes;
 #pragma unroll
           for (int k = 0; k < kTile / 32; ++k)
-            mma_f8(tmem + C::OCol, rows_desc<kD>(sv + k * 32 * kD), pd + 2 * k, kIdescO, k > 0);
+            mma_f8(tmem + C::OCol, rows_desc<kD>(sv + k * 32 * kD), pd + k * (32 * 3 * kNR / 16), kIdescO, k > 0);
           mma_commit(ofull);
           mma_commit(empty(s));
           *mma_done = it + 1;
@@ -412,7 +435,8 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       float* wred = red + wg * 80;                      // [4 warps][16 rows], for reductions
       float* wqs = wred + 64;                           // [16 rows] value of a code of Q
       const int r0 = wg * 16;
-      float m[16], l[16], acc[16];
+      float m[16];
+      f32x2 l[8], acc[8];                               // two rows each
       float vref_prev = 0.0f;
       // A wait that runs out only marks the thread: the warpgroup leaves together, at the next vote,
       // so no barrier is left waiting.
@@ -431,7 +455,8 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           tmem_ld16(at + term * kNR, t);
           tmem_ld_wait();
 #pragma unroll
-          for (int r = 0; r < 16; ++r) acc[r] = __fmaf_rn(__uint_as_float(t[r]), f, acc[r]);
+          for (int r = 0; r < 8; ++r)
+            acc[r] = fma2(pack2(__uint_as_float(t[2 * r]), __uint_as_float(t[2 * r + 1])), pack2(f, f), acc[r]);
           f *= 1.0f / kTermStep;
         }
         tc_fence_before_sync();
@@ -504,19 +529,19 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         const int rows = bad ? 0 : slot.rows, pos0 = slot.pos0, q0 = slot.q0, head = slot.head;
         if (begin) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            m[i] = -INFINITY;
-            l[i] = acc[i] = 0.0f;
-          }
+          for (int i = 0; i < 16; ++i) m[i] = kNoScore;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) l[i] = acc[i] = 0ull;
         }
         // scores of this thread's token
         const int page = tl >> p.page_shift;
         const float kf = slot.kf[page], vr = slot.vr[page];
         const int j = slot.token0 + tl;
         const bool edge = slot.token0 < slot.lo || slot.token0 + kTile > slot.hi;
-        // rows [from, to) of the warpgroup see the token
-        int from = (j - pos0) * p.G, to = rows;
-        if (p.a.window > 0) to = min(to, j - pos0 + p.a.window > 0 ? (j - pos0 + p.a.window) * p.G : 0);
+        // rows [from, to) of the warpgroup see the token; rows past the live ones may see anything
+        int from = max(j - pos0, 0) * p.G, to = 16 + r0;
+        if (p.a.window > 0)
+          to = min(to, j - pos0 + p.a.window > 0 ? min(j - pos0 + p.a.window, 64) * p.G : 0);
         if (j >= slot.hi || j < slot.lo) to = 0;
         from = min(max(from - r0, 0), 16);
         to = min(max(to - r0, 0), 16);
@@ -531,15 +556,23 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           tmem_ld16(at + kNR, t2);
           tmem_ld_wait();
           tc_fence_before_sync();
+          const f32x2 step = pack2(1.0f / kTermStep, 1.0f / kTermStep), kf2 = pack2(kf, kf);
 #pragma unroll
           for (int r = 0; r < 16; r += 4) {
             const float4 qs = *reinterpret_cast<const float4*>(wqs + r);
-            const float f[4] = {qs.x * kf, qs.y * kf, qs.z * kf, qs.w * kf};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float v = __fmaf_rn(__uint_as_float(t2[r + i]), 1.0f / kTermStep, __uint_as_float(t[r + i]));
-              sc[r + i] = (seen >> (r + i)) & 1 ? v * f[i] : -INFINITY;
+            for (int i = 0; i < 2; ++i) {
+              const int x = r + 2 * i;
+              const f32x2 v = fma2(pack2(__uint_as_float(t2[x]), __uint_as_float(t2[x + 1])), step,
+                                   pack2(__uint_as_float(t[x]), __uint_as_float(t[x + 1])));
+              const f32x2 f = mul2(i ? pack2(qs.z, qs.w) : pack2(qs.x, qs.y), kf2);
+              unpack2(mul2(v, f), sc[x], sc[x + 1]);
             }
+          }
+          if (seen != 0xFFFFu) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (!((seen >> r) & 1)) sc[r] = -INFINITY;
           }
         }
         bool grow = false;
@@ -557,38 +590,42 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           if (!(lane & 1)) wred[q * 16 + (lane >> 1)] = top;
           named_barrier_sync(1 + wg, 128);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const float t = fmaxf(fmaxf(wred[r], wred[16 + r]), fmaxf(wred[32 + r], wred[48 + r]));
-            const float mn = fmaxf(m[r], t);
-            const float alpha = m[r] == mn ? 1.0f : exp2_approx(m[r] - mn);
-            l[r] *= alpha;
-            acc[r] *= alpha;
-            m[r] = mn;
+          for (int r = 0; r < 16; r += 2) {
+            float alpha[2];
+#pragma unroll
+            for (int i = r; i < r + 2; ++i) {
+              const float t = fmaxf(fmaxf(wred[i], wred[16 + i]), fmaxf(wred[32 + i], wred[48 + i]));
+              const float mn = fmaxf(m[i], t);
+              alpha[i - r] = m[i] == mn ? 1.0f : exp2_approx(m[i] - mn);
+              m[i] = mn;
+            }
+            l[r / 2] = mul2(l[r / 2], pack2(alpha[0], alpha[1]));
+            acc[r / 2] = mul2(acc[r / 2], pack2(alpha[0], alpha[1]));
           }
         }
         if (pending) add_output(it - 1);
-        // probabilities, three E4M3 terms each; rows two by two
+        // probabilities, rounded to FP16 (11 bits, down to 2^-29), then three E4M3 terms each
+        uint32_t term[3][4];
 #pragma unroll
         for (int r = 0; r < 16; r += 2) {
-          const float p0 = exp2_approx(sc[r] - (m[r] == -INFINITY ? 0.0f : m[r]));
-          const float p1 = exp2_approx(sc[r + 1] - (m[r + 1] == -INFINITY ? 0.0f : m[r + 1]));
-          l[r] += p0;
-          l[r + 1] += p1;
-          float a = p0 * vr, b = p1 * vr;
+          float p0, p1;
+          unpack2(add2(pack2(sc[r], sc[r + 1]), pack2(-m[r], -m[r + 1])), p0, p1);
+          const f32x2 pr = pack2(exp2_approx(p0), exp2_approx(p1));
+          l[r / 2] = add2(l[r / 2], pr);
+          unpack2(mul2(pr, pack2(vr, vr)), p0, p1);
+          uint32_t h2 = pack_f16x2(p0, p1);
 #pragma unroll
-          for (int term = 0; term < 3; ++term) {
-            const uint32_t code = cvt_e4m3x2(a, b);
-            const int row = term * kNR + r0 + r;
-            st_u8(sP + swz<128>(row, tl), code);
-            st_u8(sP + swz<128>(row + 1, tl), code >> 8);
-            if (term < 2) {
-              float fa, fb;
-              e4m3x2_to_f32(code, fa, fb);
-              a = (a - fa) * kTermStep;
-              b = (b - fb) * kTermStep;
-            }
+          for (int k = 0; k < 3; ++k) {
+            const uint32_t code = take_term(h2);
+            if (r & 2) term[k][r / 4] |= code << 16;
+            else term[k][r / 4] = code;
           }
         }
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          *reinterpret_cast<uint4*>(smem + (sP - sbase) + (tl >> 3) * (3 * kNR * 8) +
+                                    (k * C::WGs + wg) * 128 + (tl & 7) * 16) =
+              make_uint4(term[k][0], term[k][1], term[k][2], term[k][3]);
         if (edge && wg == 0) {
           // V rows that no query row sees may hold anything: 0 x NaN would spread
           if (!mbar_wait(vfull(s), (it / C::Stages) & 1, abort_flag, status)) bad = true;
@@ -611,25 +648,31 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           if (!(flags & 4)) load_q(it + 1);    // while the last P V runs
           add_output(it);
           pending = false;
-          const float sum = warp_reduce16<false>(l, lane);
+          float lr[16], ar[16];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            unpack2(l[r], lr[2 * r], lr[2 * r + 1]);
+            unpack2(acc[r], ar[2 * r], ar[2 * r + 1]);
+          }
+          const float sum = warp_reduce16<false>(lr, lane);
           if (!(lane & 1)) wred[q * 16 + (lane >> 1)] = sum;
           named_barrier_sync(1 + wg, 128);
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
-            l[r] = (wred[r] + wred[16 + r]) + (wred[32 + r] + wred[48 + r]);
+            const float lsum = (wred[r] + wred[16 + r]) + (wred[32 + r] + wred[48 + r]);
             const int row = r0 + r;
             if (row >= rows || !holds_d) continue;
             if (part < 0) {
               const int i = row / p.G;
               static_cast<uint16_t*>(p.a.out)[(int64_t)(q0 + i) * p.a.out_token_stride +
                                               (int64_t)(head * p.G + row - i * p.G) * p.a.out_head_stride + d] =
-                  (uint16_t)f32_to_bf16_bits(l[r] > 0.0f || l[r] != l[r] ? acc[r] / l[r] : 0.0f);
+                  (uint16_t)f32_to_bf16_bits(lsum > 0.0f || lsum != lsum ? ar[r] / lsum : 0.0f);
             } else {
               float* o = p.parts + (size_t)part * (kNR * (kD + 2));
-              o[row * kD + d] = acc[r];
+              o[row * kD + d] = ar[r];
               if (d == 0) {
                 o[kNR * kD + 2 * row] = m[r];
-                o[kNR * kD + 2 * row + 1] = l[r];
+                o[kNR * kD + 2 * row + 1] = lsum;
               }
             }
           }
