@@ -31,6 +31,7 @@ namespace moe {
 
 constexpr float kPScale = 32.0f;           // P = 1 at the running maximum becomes 32 (up to 256)
 constexpr float kGrow = 3.0f;              // log2 by which a score may pass the maximum
+constexpr int kBatch = 8;                  // tiles whose pages are looked up together, at most
 constexpr int kItemUnits = 3;              // start and end of an item, in tiles
 constexpr float kTermStep = 32.0f;         // each further E4M3 term is scaled up by this
 constexpr float kNoScore = -3e38f;         // running maximum before the first token: finite, so that
@@ -289,94 +290,133 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
   if (cur.left > 0) {
     if (warp == 0) {
       // -------------------------------------------------------------------- producer
+      // The page table and the scales it leads to are two dependent loads, so they run ahead of the
+      // copies by two batches and one.  A batch is the next kBatch tiles of the walk (fewer with small
+      // pages): lane = tile of the batch x page of the tile, and the lanes of a tile do all its work.
       const int npg = kTile >> p.page_shift, P = 1 << p.page_shift;
-      // lane i: entry of page i of the tile; -1 where the tile needs none
-      auto entry = [&](const FewWalk<kNR>& w) {
-        if (w.left <= 0 || lane >= npg) return -1;
-        const int pg = (w.item.tile0 + w.tile) * npg + lane;
-        if ((pg << p.page_shift) >= w.item.hi || ((pg + 1) << p.page_shift) <= w.item.lo) return -1;
-        return p.a.block_table[(size_t)w.b * p.a.max_pages + pg];
+      const int group = lane / npg, pi = lane - group * npg;
+      const int batch = min(kBatch, 32 / npg);
+      const bool leader = pi == 0;
+      const int first_item = cur.b * p.a.Hkv + cur.h;
+      const bool continues = cur.tile != 0;
+      int seg = 0;
+      struct Ahead {
+        FewItem item;
+        int b, h, tile, page, part;      // page: -1 none; part: of the segment
+        int live;                        // 0: no such tile, 1: tile, 2: the CTA's last
       };
-      auto scales = [&](const FewWalk<kNR>& w, int page, float& ks, float& vs) {
+      // the lane's tile of the next batch, and its page
+      auto look = [&]() {
+        Ahead a;
+        a.live = 0;
+        a.page = -1;
+        a.part = 0;
+        for (int k = 0; k < batch && cur.left > 0; ++k) {
+          if (k == group) {
+            a.item = cur.item;
+            a.b = cur.b;
+            a.h = cur.h;
+            a.tile = cur.tile;
+            a.part = 2 * (int)blockIdx.x + (seg > 0 ? 1 : 0);
+            a.live = 1;
+          }
+          if (cur.tile == cur.item.tiles - 1) ++seg;
+          cur.next(p);
+          if (k == group && cur.left <= 0) a.live = 2;
+        }
+        if (a.live) {
+          const int pg = (a.item.tile0 + a.tile) * npg + pi;
+          if ((pg << p.page_shift) < a.item.hi && ((pg + 1) << p.page_shift) > a.item.lo)
+            a.page = p.a.block_table[(size_t)a.b * p.a.max_pages + pg];
+        }
+        return a;
+      };
+      auto scales = [&](const Ahead& a, float& ks, float& vs) {
         ks = vs = 0.0f;
-        if (page >= 0 && page < p.a.num_pages) {
-          ks = p.a.k_scale[(size_t)page * p.a.Hkv + w.h];
-          vs = p.a.v_scale[(size_t)page * p.a.Hkv + w.h];
+        if (a.page >= 0 && a.page < p.a.num_pages) {
+          ks = p.a.k_scale[(size_t)a.page * p.a.Hkv + a.h];
+          vs = p.a.v_scale[(size_t)a.page * p.a.Hkv + a.h];
         }
       };
-      // entries two tiles ahead, scales one
-      FewWalk<kNR> nxt = cur, far;
-      int page = entry(cur);
-      nxt.next(p);
-      int page1 = entry(nxt);
-      far = nxt;
-      far.next(p);
+      int tail_item = -1, tail_part = -1;
+      Ahead now = look(), nxt = look();
       float ks, vs;
-      scales(cur, page, ks, vs);
-      int head_item = -1, tail_item = -1, tail_part = -1, seg = 0;
-      bool first = true;
-      for (int it = 0; cur.left > 0; ++it) {
-        const int page2 = entry(far);
+      scales(now, ks, vs);
+      bool ok = true, more = true;
+      for (int it = 0; ok && more;) {
+        const Ahead far = look();
         float ks1, vs1;
-        scales(nxt, page1, ks1, vs1);
-        const int s = it % C::Stages;
-        bool ok = true;
-        if (lane == 0) ok = mbar_wait(empty(s), ((it / C::Stages) & 1) ^ 1, abort_flag, status);
-        if (!__shfl_sync(~0u, (int)ok, 0)) break;
-        const bool live = page >= 0 && page < p.a.num_pages;
-        const uint32_t bytes = __popc(__ballot_sync(~0u, live)) * P * kD;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(kfull(s), bytes);
-          mbar_arrive_expect_tx(vfull(s), bytes);
-        }
-        __syncwarp();
-        const uint32_t dst = sbase + s * C::StageBytes + lane * P * kD;
-        if (live) {
-          tma_load_4d(dst, &tmK, 0, 0, cur.h, page, kfull(s));
-          tma_load_4d(dst + C::HalfBytes, &tmV, 0, 0, cur.h, page, vfull(s));
-        }
+        scales(nxt, ks1, vs1);
+        const bool live = now.page >= 0 && now.page < p.a.num_pages;
         float vref = live ? vs : 0.0f;
 #pragma unroll
-        for (int d = 4; d; d >>= 1) vref = fmaxf(vref, __shfl_xor_sync(~0u, vref, d));
-        FewSlot& slot = slots[s];
-        if (lane < npg) {
-          slot.kf[lane] = ks * p.a.sm_scale * kLog2e;
-          slot.vr[lane] = vref > 0.0f ? __fdiv_rn(vs, vref) * kPScale : (vs == vs ? 0.0f : vs);
+        for (int d = kMaxTilePages / 2; d; d >>= 1) {
+          const float other = __shfl_xor_sync(~0u, vref, d);
+          if (d < npg) vref = fmaxf(vref, other);
         }
-        if (lane == 0) {
-          const bool begin = cur.tile == 0, end = cur.tile == cur.item.tiles - 1;
-          const bool last = nxt.left <= 0;
-          const int item = cur.b * p.a.Hkv + cur.h;
-          slot.vref = vref;
-          slot.token0 = (cur.item.tile0 + cur.tile) * kTile;
-          slot.lo = cur.item.lo;
-          slot.hi = cur.item.hi;
-          slot.pos0 = cur.item.L - cur.item.n;
-          slot.rows = cur.item.n * p.G;
-          slot.q0 = cur.item.q0;
-          slot.head = cur.h;
-          slot.flags = (end || last ? 2 : 0) | (last ? 4 : 0);
-          if (first && !begin) head_item = item;
-          // the segment's part of the workspace; an item that lies wholly in this CTA needs none
-          const int part = 2 * (int)blockIdx.x + (seg > 0 ? 1 : 0);
-          slot.part = end && head_item != item ? -1 : part;
-          if (last && !end && head_item != item) {
-            tail_item = item;
-            tail_part = part;
+        const uint32_t pages = __ballot_sync(~0u, live);
+        const uint32_t bytes = __popc((pages >> (group * npg)) & ((1u << npg) - 1)) * P * kD;
+        const float kf = ks * p.a.sm_scale * kLog2e;
+        const float vr = vref > 0.0f ? __fdiv_rn(vs, vref) * kPScale : (vs == vs ? 0.0f : vs);
+        for (int k = 0; k < batch; ++k) {
+          if (!__any_sync(~0u, group == k && now.live)) break;
+          const int s = it % C::Stages;
+          const bool mine = group == k;
+          bool here = true;
+          if (mine && leader) {
+            here = mbar_wait(empty(s), ((it / C::Stages) & 1) ^ 1, abort_flag, status);
+            if (here) {
+              mbar_arrive_expect_tx(kfull(s), bytes);
+              mbar_arrive_expect_tx(vfull(s), bytes);
+            }
           }
-          mbar_arrive(ifull(s));
+          ok = __all_sync(~0u, here);
+          if (!ok) break;
+          FewSlot& slot = slots[s];
+          if (mine) {
+            if (live) {
+              const uint32_t dst = sbase + s * C::StageBytes + pi * P * kD;
+              tma_load_4d(dst, &tmK, 0, 0, now.h, now.page, kfull(s));
+              tma_load_4d(dst + C::HalfBytes, &tmV, 0, 0, now.h, now.page, vfull(s));
+            }
+            slot.kf[pi] = kf;
+            slot.vr[pi] = vr;
+            if (leader) {
+              const bool end = now.tile == now.item.tiles - 1, last = now.live == 2;
+              const int item = now.b * p.a.Hkv + now.h;
+              const bool continued = continues && item == first_item;
+              slot.vref = vref;
+              slot.token0 = (now.item.tile0 + now.tile) * kTile;
+              slot.lo = now.item.lo;
+              slot.hi = now.item.hi;
+              slot.pos0 = now.item.L - now.item.n;
+              slot.rows = now.item.n * p.G;
+              slot.q0 = now.item.q0;
+              slot.head = now.h;
+              slot.flags = (end || last ? 2 : 0) | (last ? 4 : 0);
+              // an item that lies wholly in this CTA needs no part of the workspace
+              slot.part = end && !continued ? -1 : now.part;
+              if (last && !end && !continued) {
+                tail_item = item;
+                tail_part = now.part;
+              }
+            }
+          }
+          __syncwarp();
+          if (mine && leader) mbar_arrive(ifull(s));
+          ++it;
+          ++issued;
         }
-        if (cur.tile == cur.item.tiles - 1) ++seg;
-        first = false;
-        ++issued;
-        cur = nxt;
+        more = !__any_sync(~0u, now.live == 2);
+        now = nxt;
         nxt = far;
-        far.next(p);
-        page = page1;
-        page1 = page2;
         ks = ks1;
         vs = vs1;
       }
+      // the lane that met the CTA's last tile knows what it leaves open
+      tail_item = __reduce_max_sync(~0u, tail_item);
+      tail_part = __reduce_max_sync(~0u, tail_part);
+      const int head_item = continues ? first_item : -1;
       if (lane == 0) p.meta[blockIdx.x] = make_int4(head_item, tail_item, tail_part, 0);
     } else if (warp == 1) {
       // ------------------------------------------------------------------------- MMA
