@@ -348,16 +348,9 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         float ks1, vs1;
         scales(nxt, ks1, vs1);
         const bool live = now.page >= 0 && now.page < p.a.num_pages;
-        float vref = live ? vs : 0.0f;
-#pragma unroll
-        for (int d = kMaxTilePages / 2; d; d >>= 1) {
-          const float other = __shfl_xor_sync(~0u, vref, d);
-          if (d < npg) vref = fmaxf(vref, other);
-        }
         const uint32_t pages = __ballot_sync(~0u, live);
         const uint32_t bytes = __popc((pages >> (group * npg)) & ((1u << npg) - 1)) * P * kD;
-        const float kf = ks * p.a.sm_scale * kLog2e;
-        const float vr = vref > 0.0f ? __fdiv_rn(vs, vref) * kPScale : (vs == vs ? 0.0f : vs);
+        float kf = 0.0f, vr = 0.0f, vref = 0.0f;
         for (int k = 0; k < batch; ++k) {
           if (!__any_sync(~0u, group == k && now.live)) break;
           const int s = it % C::Stages;
@@ -379,6 +372,19 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
               tma_load_4d(dst, &tmK, 0, 0, now.h, now.page, kfull(s));
               tma_load_4d(dst + C::HalfBytes, &tmV, 0, 0, now.h, now.page, vfull(s));
             }
+          }
+          if (k == 0) {
+            // the scales are needed only now that the batch's first copies are on their way
+            vref = live ? vs : 0.0f;
+#pragma unroll
+            for (int d = kMaxTilePages / 2; d; d >>= 1) {
+              const float other = __shfl_xor_sync(~0u, vref, d);
+              if (d < npg) vref = fmaxf(vref, other);
+            }
+            kf = ks * p.a.sm_scale * kLog2e;
+            vr = vref > 0.0f ? __fdiv_rn(vs, vref) * kPScale : (vs == vs ? 0.0f : vs);
+          }
+          if (mine) {
             slot.kf[pi] = kf;
             slot.vr[pi] = vr;
             if (leader) {
@@ -487,18 +493,19 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           return;
         }
         tc_fence_after_sync();
-        uint32_t t[16];
+        uint32_t t[3][16];
         const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + C::OCol + r0;
-        float f = vref_prev * (1.0f / kPScale);
 #pragma unroll
-        for (int term = 0; term < 3; ++term) {
-          tmem_ld16(at + term * kNR, t);
-          tmem_ld_wait();
+        for (int k = 0; k < 3; ++k) tmem_ld16(at + k * kNR, t[k]);
+        tmem_ld_wait();
+        const float f = vref_prev * (1.0f / kPScale);
+        const f32x2 f2 = pack2(f, f), step = pack2(1.0f / kTermStep, 1.0f / kTermStep);
+        auto pair = [&](int k, int r) {
+          return pack2(__uint_as_float(t[k][2 * r]), __uint_as_float(t[k][2 * r + 1]));
+        };
 #pragma unroll
-          for (int r = 0; r < 8; ++r)
-            acc[r] = fma2(pack2(__uint_as_float(t[2 * r]), __uint_as_float(t[2 * r + 1])), pack2(f, f), acc[r]);
-          f *= 1.0f / kTermStep;
-        }
+        for (int r = 0; r < 8; ++r)
+          acc[r] = fma2(fma2(fma2(pair(2, r), step, pair(1, r)), step, pair(0, r)), f2, acc[r]);
         tc_fence_before_sync();
       };
       // Q of the segment that begins with tile `it`: 8 threads a row, D / 8 values each, two E4M3 terms.

@@ -7,9 +7,13 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import NamedTuple
 
-from . import MOE_ERR_INVALID_ARG, SCALE_FP32, MoeError, _check, _stream, load_library
+import torch
+
+from . import MOE_ERR_INVALID_ARG, SCALE_FP32, MoeError, _check, load_library
+from . import _stream as _given_stream
 
 ROPE_HALF = 0
 ROPE_INTERLEAVED = 1
@@ -49,12 +53,18 @@ class KVAttentionArgs(ctypes.Structure):
                                   "max_q", "window")] + [("sm_scale", _F)]
 
 
+# The C structures' layouts for struct.pack: a decode step is a handful of short calls, and packing the
+# fields is several times quicker than filling a ctypes structure (tests hold the two layouts together).
+_PACK_TABLES = struct.Struct("@16P6i")
+_PACK_APPEND = struct.Struct("@13P8q11i0P")
+_PACK_ATTENTION = struct.Struct("@9P4q10if0P")
+
 SIGNATURES = {
-    "moe_kv_tables": (_I, [ctypes.POINTER(KVTablesArgs), _VP]),
+    "moe_kv_tables": (_I, [_VP, _VP]),
     "moe_rope_table": (_I, [_VP, _I, _I, _D, _I, _D, _D, _D, _I, _F, _VP]),
-    "moe_rope_append": (_I, [ctypes.POINTER(RopeAppendArgs), _VP]),
+    "moe_rope_append": (_I, [_VP, _VP]),
     "moe_kv_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
-    "moe_kv_attention": (_I, [ctypes.POINTER(KVAttentionArgs), _VP, _SZ, _VP]),
+    "moe_kv_attention": (_I, [_VP, _VP, _SZ, _VP]),
 }
 
 
@@ -82,13 +92,23 @@ class KVCache(NamedTuple):
     v_scale: object
 
 
+def _stream(stream):
+    """The stream's handle; torch's current one through the raw handle, without building an object
+    (3 us of a call that takes 10)."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return _given_stream(stream)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _bad(what: str):
     raise MoeError(MOE_ERR_INVALID_ARG, what)
 
 
 def _i32(name: str, t, shape):
-    import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         _bad(f"{name}: a contiguous int32 tensor of shape {shape} is needed")
     return t.data_ptr()
 
@@ -100,7 +120,6 @@ def max_runs(max_tokens: int, page_size: int, num_requests: int) -> int:
 
 def alloc_kv_cache(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int,
                    device="cuda") -> KVCache:
-    import torch
     shape = (num_pages, num_kv_heads, page_size, head_dim)
     code = [torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2)]
     scale = [torch.zeros(shape[:2], dtype=torch.float32, device=device) for _ in range(2)]
@@ -111,7 +130,6 @@ def alloc_kv_tables(num_requests: int, max_pages: int, num_pages: int, page_size
                     max_tokens: int, device="cuda") -> KVTables:
     """A set of tables for `num_requests` requests and steps of up to `max_tokens` tokens: all pages
     free, no request holds any."""
-    import torch
     i32 = dict(dtype=torch.int32, device=device)
     runs = max_runs(max_tokens, page_size, num_requests)
     return KVTables(
@@ -137,17 +155,17 @@ def kv_tables(cur_len, new_len, block_table, free_list, free_count, *, page_size
     T, R = out.slot.shape[0], out.run_tok.shape[0]
     if max_tokens is not None and max_tokens != T:
         _bad("kv_tables: out holds another number of tokens than max_tokens")
-    a = KVTablesArgs(
-        _i32("cur_len", cur_len, (B,)), _i32("new_len", new_len, (B,)),
-        _i32("block_table", block_table, (B, W)), _i32("free_list", free_list, (N,)),
-        _i32("free_count", free_count, (1,)), _i32("out.block_table", out.block_table, (B, W)),
-        _i32("out.free_list", out.free_list, (N,)), _i32("out.free_count", out.free_count, (1,)),
-        _i32("out.kv_len", out.kv_len, (B,)), _i32("out.tok_start", out.tok_start, (B + 1,)),
-        _i32("out.slot", out.slot, (T,)), _i32("out.position", out.position, (T,)),
-        _i32("out.request", out.request, (T,)), _i32("out.run_tok", out.run_tok, (R,)),
-        _i32("out.run_len", out.run_len, (R,)), _i32("out.info", out.info, (4,)),
-        B, W, N, page_size, T, R)
-    _check(load_library().moe_kv_tables(ctypes.byref(a), _stream(stream)), "moe_kv_tables")
+    b, t, r, one, table, pool = (B,), (T,), (R,), (1,), (B, W), (N,)
+    a = _PACK_TABLES.pack(
+        _i32("cur_len", cur_len, b), _i32("new_len", new_len, b), _i32("block_table", block_table, table),
+        _i32("free_list", free_list, pool), _i32("free_count", free_count, one),
+        _i32("out.block_table", out.block_table, table), _i32("out.free_list", out.free_list, pool),
+        _i32("out.free_count", out.free_count, one), _i32("out.kv_len", out.kv_len, b),
+        _i32("out.tok_start", out.tok_start, (B + 1,)), _i32("out.slot", out.slot, t),
+        _i32("out.position", out.position, t), _i32("out.request", out.request, t),
+        _i32("out.run_tok", out.run_tok, r), _i32("out.run_len", out.run_len, r),
+        _i32("out.info", out.info, (4,)), B, W, N, page_size, T, R)
+    _check(load_library().moe_kv_tables(a, _stream(stream)), "moe_kv_tables")
     return out
 
 
@@ -155,7 +173,6 @@ def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, *, scaling: in
                factor: float = 1.0, low: float = 1.0, high: float = 32.0, original_len: int = 4096,
                magnitude: float = 1.0, out=None, device="cuda", stream=None):
     """cos and sin of every position, fp32 [max_pos, rot_dim / 2, 2] (moe_rope_table)."""
-    import torch
     if out is None:
         out = torch.empty((max_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
     elif out.dtype != torch.float32 or tuple(out.shape) != (max_pos, rot_dim // 2, 2) or not out.is_contiguous():
@@ -168,23 +185,24 @@ def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, *, scaling: in
 
 def _heads(name: str, t, T: int, H: int, D: int):
     """Pointer, token stride and head stride of a BF16 tensor [T, H, D] with contiguous heads."""
-    import torch
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, H, D) or (t.stride(2) != 1 and t.numel()):
-        _bad(f"{name}: a bfloat16 tensor of shape {(T, H, D)} with contiguous heads is needed")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    if t.dtype is not torch.bfloat16 or t.shape != (T, H, D):
+        _bad(f"{name}: a bfloat16 tensor of shape {(T, H, D)} is needed")
+    st, sh, sd = t.stride()
+    if sd != 1:
+        _bad(f"{name}: the values of a head have to be contiguous")
+    return t.data_ptr(), st, sh
 
 
 def _cache(cache: KVCache):
     """Pointers of the cache's tensors and (num_pages, Hkv, page_size, D)."""
-    import torch
     kc, vc, ks, vs = cache
-    shape = tuple(kc.shape)
-    if (len(shape) != 4 or tuple(vc.shape) != shape or kc.element_size() != 1 or vc.element_size() != 1
-            or tuple(ks.shape) != shape[:2] or tuple(vs.shape) != shape[:2]
-            or ks.dtype != torch.float32 or vs.dtype != torch.float32
-            or not (kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous())):
+    shape = kc.shape
+    if (len(shape) != 4 or vc.shape != shape or kc.element_size() != 1 or vc.element_size() != 1
+            or ks.shape != shape[:2] or vs.shape != ks.shape or ks.dtype is not torch.float32
+            or vs.dtype is not torch.float32 or not (kc.is_contiguous() and vc.is_contiguous()
+                                                     and ks.is_contiguous() and vs.is_contiguous())):
         _bad("cache: contiguous codes [num_pages, Hkv, page_size, D] and fp32 scales [num_pages, Hkv] are needed")
-    return (kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr()), shape
+    return kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape
 
 
 def rope_append(q, k, v, rope, tables: KVTables, cache: KVCache, *, layout: int = ROPE_HALF,
@@ -192,13 +210,12 @@ def rope_append(q, k, v, rope, tables: KVTables, cache: KVCache, *, layout: int 
     """Rotate q and k [T, heads, D] by the tables' positions, write k and v to the cache and return the
     rotated q (moe_rope_append).  rope: rope_table's result, or None for no rotation; q None: cache
     write only; q_out may be q.  T is the tables' token capacity."""
-    import torch
-    (kc, vc, ks, vs), (N, Hkv, P, D) = _cache(cache)
+    kc, vc, ks, vs, (N, Hkv, P, D) = _cache(cache)
     T, R = tables.slot.shape[0], tables.run_tok.shape[0]
     rot = max_pos = 0
-    rp = None
+    rp = 0
     if rope is not None:
-        if rope.dtype != torch.float32 or rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous():
+        if rope.dtype is not torch.float32 or rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous():
             _bad("rope: a contiguous fp32 tensor [max_pos, rot_dim / 2, 2] is needed")
         max_pos, rot, rp = rope.shape[0], 2 * rope.shape[1], rope.data_ptr()
     Hq = qp = op = qt = qh = ot = oh = 0
@@ -210,11 +227,12 @@ def rope_append(q, k, v, rope, tables: KVTables, cache: KVCache, *, layout: int 
         op, ot, oh = _heads("q_out", q_out, T, Hq, D)
     kp, kt, kh = _heads("k", k, T, Hkv, D)
     vp, vt, vh = _heads("v", v, T, Hkv, D)
-    a = RopeAppendArgs(qp, kp, vp, op, rp, _i32("position", tables.position, (T,)),
-                       _i32("slot", tables.slot, (T,)), _i32("run_tok", tables.run_tok, (R,)),
-                       _i32("run_len", tables.run_len, (R,)), kc, vc, ks, vs, qt, qh, kt, kh, vt, vh,
-                       ot, oh, T, Hq, Hkv, D, P, N, R, rot, max_pos, layout, scale_fmt)
-    _check(load_library().moe_rope_append(ctypes.byref(a), _stream(stream)), "moe_rope_append")
+    t, r = (T,), (R,)
+    a = _PACK_APPEND.pack(qp, kp, vp, op, rp, _i32("position", tables.position, t),
+                          _i32("slot", tables.slot, t), _i32("run_tok", tables.run_tok, r),
+                          _i32("run_len", tables.run_len, r), kc, vc, ks, vs, qt, qh, kt, kh, vt, vh,
+                          ot, oh, T, Hq, Hkv, D, P, N, R, rot, max_pos, layout, scale_fmt)
+    _check(load_library().moe_rope_append(a, _stream(stream)), "moe_rope_append")
     return q_out
 
 
@@ -225,7 +243,6 @@ def kv_attention_workspace_bytes(num_heads: int, num_kv_heads: int, head_dim: in
 def alloc_kv_attention_workspace(num_heads: int, num_kv_heads: int, head_dim: int, max_q: int,
                                  device="cuda"):
     """A zeroed workspace for kv_attention calls with these heads and up to max_q tokens a request."""
-    import torch
     n = kv_attention_workspace_bytes(num_heads, num_kv_heads, head_dim, max_q)
     return torch.zeros(max(256, n), dtype=torch.uint8, device=device)
 
@@ -236,18 +253,18 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, tok_start, workspace, *
     rows [tok_start[b], tok_start[b+1]) of q and the last ones of its kv_len[b] cached tokens.  max_q
     bounds the tokens of one request; sm_scale defaults to D^-0.5; window > 0 limits how far back a
     token sees."""
-    import torch
-    (kc, vc, ks, vs), (N, Hkv, P, D) = _cache(cache)
+    kc, vc, ks, vs, (N, Hkv, P, D) = _cache(cache)
     T, Hq = q.shape[0], q.shape[1]
     B, W = block_table.shape
     if out is None:
         out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
     qp, qt, qh = _heads("q", q, T, Hq, D)
     op, ot, oh = _heads("out", out, T, Hq, D)
-    a = KVAttentionArgs(qp, kc, vc, ks, vs, _i32("block_table", block_table, (B, W)),
-                        _i32("kv_len", kv_len, (B,)), _i32("tok_start", tok_start, (B + 1,)), op, qt, qh,
-                        ot, oh, T, B, Hq, Hkv, D, P, N, W, max_q, window,
-                        1.0 / math.sqrt(D) if sm_scale is None else sm_scale)
-    _check(load_library().moe_kv_attention(ctypes.byref(a), workspace.data_ptr(), workspace.numel(),
-                                           _stream(stream)), "moe_kv_attention")
+    b = (B,)
+    a = _PACK_ATTENTION.pack(qp, kc, vc, ks, vs, _i32("block_table", block_table, (B, W)),
+                             _i32("kv_len", kv_len, b), _i32("tok_start", tok_start, (B + 1,)), op, qt, qh,
+                             ot, oh, T, B, Hq, Hkv, D, P, N, W, max_q, window,
+                             1.0 / math.sqrt(D) if sm_scale is None else sm_scale)
+    _check(load_library().moe_kv_attention(a, workspace.data_ptr(), workspace.numel(), _stream(stream)),
+           "moe_kv_attention")
     return out

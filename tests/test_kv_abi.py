@@ -130,3 +130,14 @@ def test_binding_refuses_wrong_tensors():
         moe.kv_attention(q, cache, t.block_table, t.kv_len, t.tok_start[:-1], ws, max_q=1)
     with pytest.raises(moe.MoeError):
         moe.kv_tables(t.kv_len, t.kv_len, t.block_table, t.free_list, t.free_count, page_size=16)
+
+
+def test_packed_arguments_match_the_structures():
+    """The binding packs its arguments with struct formats; they have to be the C structures' layouts."""
+    from block_fp8_mixture_gb300 import kv
+    for cls, fmt in ((moe.KVTablesArgs, kv._PACK_TABLES), (moe.RopeAppendArgs, kv._PACK_APPEND),
+                     (moe.KVAttentionArgs, kv._PACK_ATTENTION)):
+        values = [i + 1 for i in range(len(cls._fields_))]
+        got = cls.from_buffer_copy(fmt.pack(*values))
+        assert fmt.size == ctypes.sizeof(cls)
+        assert [getattr(got, n) for n, _ in cls._fields_] == values
