@@ -37,7 +37,7 @@ constexpr float kPromptGrow = 8.0f;           // log2 by which a row may pass it
 constexpr float kPromptBias = 4.0f;           // log2 of p' at the maximum
 constexpr int kMinPieceTiles = 4;             // a piece of a cut block has at least this many tiles
 // registers of the four warpgroups, launched with 128 each
-constexpr int kRegsIssue = 56, kRegsWiden = 72, kRegsSoftmax = 192;
+constexpr int kRegsIssue = 56, kRegsWiden = 56, kRegsSoftmax = 200;
 static_assert(kRegsIssue + kRegsWiden + 2 * kRegsSoftmax <= 512, "register split must fit the launch");
 
 template <int kD>
@@ -233,6 +233,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 template <int kRegs>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -266,10 +272,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   auto iempty = [&](int s) { return bar0 + 8u * (28 + s); };
   auto qfull = [&](int w) { return bar0 + 8u * (32 + w); };
   auto sfull = [&](int w) { return bar0 + 8u * (34 + w); };
-  auto pfull = [&](int w) { return bar0 + 8u * (36 + w); };
-  auto ofull = [&](int w) { return bar0 + 8u * (38 + w); };
-  const uint32_t drain = bar0 + 8u * 40;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * 41);
+  auto pfull = [&](int w, int half) { return bar0 + 8u * (36 + 2 * w + half); };
+  auto ofull = [&](int w) { return bar0 + 8u * (40 + w); };
+  const uint32_t drain = bar0 + 8u * 42;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * 43);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* k_done = reinterpret_cast<volatile int*>(tmem_slot + 2);
   volatile int* v_done = reinterpret_cast<volatile int*>(tmem_slot + 3);
@@ -290,7 +296,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     for (int w = 0; w < 2; ++w) {
       mbar_init(qfull(w), 4);
       mbar_init(sfull(w), 1);
-      mbar_init(pfull(w), 4);
+      mbar_init(pfull(w, 0), 4);
+      mbar_init(pfull(w, 1), 4);
       mbar_init(ofull(w), 1);
     }
     mbar_init(drain, 1);
@@ -398,17 +405,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       auto k_ready = [&](int tile) {
         return mbar_wait(kfull(tile % C::KStages), (tile / C::KStages) & 1, abort_flag, status);
       };
+      // P arrives in two halves of the tile's tokens: the product of the first runs while the softmax
+      // warps form the second
       auto output = [&](int w, int tile, bool first) {
-        if (!mbar_wait(pfull(w), tile & 1, abort_flag, status)) return false;
-        tc_fence_after_sync();
         const uint32_t wt = sW + tile % C::WStages * C::WBytes;
         // V in FP16: rows of 64 values (128 bytes), the second half of the values 16 KB further
         uint64_t vd = make_sdesc_sw128(wt, 1024);
         vd = (vd & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)((kTile * 128) >> 4) << 16);
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_f16_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, vd + k * (16 * 128 / 16), kIdescO,
-                     !first || k > 0);
+        for (int half = 0; half < 2; ++half) {
+          if (!mbar_wait(pfull(w, half), tile & 1, abort_flag, status)) return false;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int k = 4 * half; k < 4 * half + 4; ++k)
+            mma_f16_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, vd + k * (16 * 128 / 16), kIdescO,
+                       !first || k > 0);
+        }
         mma_commit(ofull(w));
         if (w == 1) mma_commit(wempty(tile % C::WStages));
         return true;
@@ -595,25 +607,40 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
         tmem_ld_wait();
-        float* x = reinterpret_cast<float*>(s);
+        auto x = [&](int i) { return __uint_as_float(s[i]); };
+        // x f + lv is the score plus log2 of the V scale, in log2 units
+        float f[8], lv[8];
+#pragma unroll
+        for (int g = 0; g < 8; g += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(slot.kf + g);
+          const float4 b = *reinterpret_cast<const float4*>(slot.lv + g);
+          f[g] = a.x * qs, f[g + 1] = a.y * qs, f[g + 2] = a.z * qs, f[g + 3] = a.w * qs;
+          lv[g] = b.x, lv[g + 1] = b.y, lv[g + 2] = b.z, lv[g + 3] = b.w;
+        }
         if (edge) {
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
-            const float f = slot.kf[g] * qs, lv = slot.lv[g];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int j = token0 + 16 * g + i;
-              x[16 * g + i] = j >= see_lo && j < see_hi ? __fmaf_rn(x[16 * g + i], f, lv) : -INFINITY;
+            for (int i = 16 * g; i < 16 * g + 16; ++i) {
+              const int j = token0 + i;
+              s[i] = __float_as_uint(j >= see_lo && j < see_hi ? __fmaf_rn(x(i), f[g], lv[g]) : -INFINITY);
             }
+            f[g] = 1.0f;
+            lv[g] = 0.0f;
           }
         }
         float top = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
-          float m = x[16 * g];
+          float m = max3(x(16 * g), x(16 * g + 1), x(16 * g + 2));
+          float m2 = max3(x(16 * g + 3), x(16 * g + 4), x(16 * g + 5));
 #pragma unroll
-          for (int i = 1; i < 16; ++i) m = fmaxf(m, x[16 * g + i]);
-          top = fmaxf(top, edge ? m : __fmaf_rn(m, slot.kf[g] * qs, slot.lv[g]));
+          for (int i = 16 * g + 6; i < 16 * g + 14; i += 4) {
+            m = max3(m, x(i), x(i + 1));
+            m2 = max3(m2, x(i + 2), x(i + 3));
+          }
+          m = max3(m, x(16 * g + 14), x(16 * g + 15));
+          top = fmaxf(top, __fmaf_rn(fmaxf(m, m2), f[g], lv[g]));
         }
         if (__any_sync(~0u, top > M + kPromptGrow)) {
           const float mn = fmaxf(M, top);
@@ -640,28 +667,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         const float base = kPromptBias - (M == -INFINITY ? 0.0f : M);
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const float f = edge ? 1.0f : slot.kf[g] * qs;
-          const float add = edge ? base : slot.lv[g] + base;
-          float sum0 = 0.0f, sum1 = 0.0f;
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float p0 = exp2_approx(__fmaf_rn(x[16 * g + i], f, add));
-            const float p1 = exp2_approx(__fmaf_rn(x[16 * g + i + 1], f, add));
-            sum0 += p0;
-            sum1 += p1;
-            s[8 * g + i / 2] = pack_f16x2(p0, p1);
+          for (int g = 4 * half; g < 4 * half + 4; ++g) {
+            const f32x2 f2 = pack2(f[g], f[g]), add = pack2(lv[g] + base, lv[g] + base);
+            f32x2 sum = 0ull;
+#pragma unroll
+            for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+              float p0, p1;
+              unpack2(fma2(pack2(x(i), x(i + 1)), f2, add), p0, p1);
+              p0 = exp2_approx(p0);
+              p1 = exp2_approx(p1);
+              sum = add2(sum, pack2(p0, p1));
+              s[i / 2] = pack_f16x2(p0, p1);
+            }
+            float s0, s1;
+            unpack2(sum, s0, s1);
+            l = __fmaf_rn(s0 + s1, slot.iv[g], l);
           }
-          l = __fmaf_rn(sum0 + sum1, slot.iv[g], l);
-        }
-        tmem_st32(tS, s);
-        tmem_st32(tS + 32, s + 32);
-        tmem_st_wait();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(iempty(si));
-          mbar_arrive(pfull(wg));
+          tmem_st32(tS + 32 * half, s + 32 * half);
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if (half == 1) mbar_arrive(iempty(si));
+            mbar_arrive(pfull(wg, half));
+          }
         }
       }
       if (!ok) break;
