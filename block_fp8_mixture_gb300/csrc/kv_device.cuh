@@ -57,6 +57,42 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// The issuing warp stays converged and one elected lane issues: the descriptors then stay in uniform
+// registers.  Issued from a branch that only one lane takes, every product costs 110 to 170 cycles of
+// moves, more than the 65 that a 128 x 128 one takes to execute.  (elect.sync names the same lane every
+// time, so that lane's commits cover its products.)
+#define KV_ELECT "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t@e "
+
+// D[tmem] (+)= A[smem] * B[smem]: E4M3, fp32 sums.
+__device__ __forceinline__ void mma_f8_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(KV_ELECT "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+               : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: FP16 operands, fp32 sums.
+__device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(KV_ELECT "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+               "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+               : "memory");
+}
+
+// Arrive on `bar` when the elected lane's products so far are complete.
+__device__ __forceinline__ void mma_commit_warp(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+
+// A wait of the whole warp; the same answer in every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                               int* status) {
+  return __all_sync(~0u, mbar_wait(bar, parity, abort_flag, status));
+}
+
 // Offset of byte x of row r in K-major rows of kRow bytes with the 128- or 64-byte swizzle.
 template <int kRow>
 __device__ __forceinline__ uint32_t swz(int r, int x) {

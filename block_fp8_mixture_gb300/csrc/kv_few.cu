@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       if (lane == 0) p.meta[blockIdx.x] = make_int4(head_item, tail_item, tail_part, 0);
     } else if (warp == 1) {
       // ------------------------------------------------------------------------- MMA
-      if (lane == 0) {
+      {
         constexpr uint32_t kIdescS = make_idesc_e4m3(kTile, 2 * kNR);
         constexpr uint32_t kIdescO = make_idesc_e4m3(kD, 3 * kNR) | (3u << 15);   // both MN-major
         const uint64_t qd = rows_desc<kD>(sQ), pd = p_desc<kNR>(sP);
@@ -434,38 +434,38 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         const bool ok = true;
         auto scores = [&](int it) {
           const int s = it % C::Stages;
-          if (!mbar_wait(kfull(s), (it / C::Stages) & 1, abort_flag, status)) return false;
+          if (!mbar_wait_warp(kfull(s), (it / C::Stages) & 1, abort_flag, status)) return false;
           tc_fence_after_sync();
           const uint64_t kd = rows_desc<kD>(sbase + s * C::StageBytes);
           const uint32_t d = tmem + (it & 1) * C::SCols;
 #pragma unroll
-          for (int k = 0; k < kD / 32; ++k) mma_f8(d, kd + 2 * k, qd + 2 * k, kIdescS, k > 0);
-          mma_commit(sfull(it & 1));
+          for (int k = 0; k < kD / 32; ++k) mma_f8_warp(d, kd + 2 * k, qd + 2 * k, kIdescS, k > 0);
+          mma_commit_warp(sfull(it & 1));
           return true;
         };
         for (int it = 0; ok; ++it) {
           const int s = it % C::Stages;
           if (it == 0) {
-            if (!mbar_wait(qfull, segs & 1, abort_flag, status) || !scores(0)) break;
+            if (!mbar_wait_warp(qfull, segs & 1, abort_flag, status) || !scores(0)) break;
             ++segs;
           }
-          if (!mbar_wait(ifull(s), (it / C::Stages) & 1, abort_flag, status)) break;
+          if (!mbar_wait_warp(ifull(s), (it / C::Stages) & 1, abort_flag, status)) break;
           const int flags = *reinterpret_cast<volatile int*>(&slots[s].flags);
           const bool more = !(flags & 4), same = !(flags & 2);
           if (same && !scores(it + 1)) break;
-          if (!mbar_wait(pfull, it & 1, abort_flag, status) ||
-              !mbar_wait(vfull(s), (it / C::Stages) & 1, abort_flag, status))
+          if (!mbar_wait_warp(pfull, it & 1, abort_flag, status) ||
+              !mbar_wait_warp(vfull(s), (it / C::Stages) & 1, abort_flag, status))
             break;
           tc_fence_after_sync();
           const uint32_t sv = sbase + s * C::StageBytes + C::HalfBytes;
 #pragma unroll
           for (int k = 0; k < kTile / 32; ++k)
-            mma_f8(tmem + C::OCol, rows_desc<kD>(sv + k * 32 * kD), pd + k * (32 * 3 * kNR / 16), kIdescO, k > 0);
-          mma_commit(ofull);
-          mma_commit(empty(s));
-          *mma_done = it + 1;
+            mma_f8_warp(tmem + C::OCol, rows_desc<kD>(sv + k * 32 * kD), pd + k * (32 * 3 * kNR / 16), kIdescO, k > 0);
+          mma_commit_warp(ofull);
+          mma_commit_warp(empty(s));
+          if (lane == 0) *mma_done = it + 1;
           if (more && !same) {
-            if (!mbar_wait(qfull, segs & 1, abort_flag, status) || !scores(it + 1)) break;
+            if (!mbar_wait_warp(qfull, segs & 1, abort_flag, status) || !scores(it + 1)) break;
             ++segs;
           }
           if (!more) break;
@@ -744,8 +744,8 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       }
     }
   };
-  if (warp == 1 && lane == 0) {
-    mma_commit(drain);
+  if (warp == 1) {
+    mma_commit_warp(drain);
     drain_wait(drain, 0);
   }
   if (warp == 0 && lane == 0 && *abort_flag) {

@@ -210,17 +210,6 @@ __global__ void __launch_bounds__(1024) k_prompt_plan(const PromptParams p) {
   }
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]: FP16 operands, fp32 sums, issued by one thread.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -382,7 +371,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           vs = vs1;
         }
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ------------------------------------------------------------------------- MMA
       constexpr uint32_t kIdescS = make_idesc_e4m3(128, kTile);
       // D fp32, A and B FP16, B MN-major, 128 x kD
@@ -397,13 +386,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const uint64_t qd = rows_desc<kD>(sQ + (2 * w + term) * C::QTerm);
 #pragma unroll
           for (int k = 0; k < kD / 32; ++k)
-            mma_f8(tmem + 128 * w, qd + 2 * k, kd + 2 * k, kIdescS, term + k > 0);
+            mma_f8_warp(tmem + 128 * w, qd + 2 * k, kd + 2 * k, kIdescS, term + k > 0);
         }
-        mma_commit(sfull(w));
-        if (w == 1) mma_commit(kempty(tile % C::KStages));
+        mma_commit_warp(sfull(w));
+        if (w == 1) mma_commit_warp(kempty(tile % C::KStages));
       };
       auto k_ready = [&](int tile) {
-        return mbar_wait(kfull(tile % C::KStages), (tile / C::KStages) & 1, abort_flag, status);
+        return mbar_wait_warp(kfull(tile % C::KStages), (tile / C::KStages) & 1, abort_flag, status);
       };
       // P arrives in two halves of the tile's tokens: the product of the first runs while the softmax
       // warps form the second
@@ -414,26 +403,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         vd = (vd & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)((kTile * 128) >> 4) << 16);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!mbar_wait(pfull(w, half), tile & 1, abort_flag, status)) return false;
+          if (!mbar_wait_warp(pfull(w, half), tile & 1, abort_flag, status)) return false;
           tc_fence_after_sync();
 #pragma unroll
           for (int k = 4 * half; k < 4 * half + 4; ++k)
-            mma_f16_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, vd + k * (16 * 128 / 16), kIdescO,
+            mma_f16_ts_warp(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, vd + k * (16 * 128 / 16), kIdescO,
                        !first || k > 0);
         }
-        mma_commit(ofull(w));
-        if (w == 1) mma_commit(wempty(tile % C::WStages));
+        mma_commit_warp(ofull(w));
+        if (w == 1) mma_commit_warp(wempty(tile % C::WStages));
         return true;
       };
       PromptWork w;
       bool have = prompt_work(p, blocks, 0, w);
       if (have) {
-        ok = mbar_wait(qfull(0), 0, abort_flag, status) && k_ready(0);
+        ok = mbar_wait_warp(qfull(0), 0, abort_flag, status) && k_ready(0);
         if (ok) {
           tc_fence_after_sync();
           scores(0, 0);
         }
-        ok = ok && mbar_wait(qfull(1), 0, abort_flag, status);
+        ok = ok && mbar_wait_warp(qfull(1), 0, abort_flag, status);
         if (ok) {
           tc_fence_after_sync();
           scores(1, 0);
@@ -442,7 +431,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       while (ok && have) {
         const int nt = w.t1 - w.t0;
         for (int t = 0; ok && t < nt; ++t, ++it) {
-          if (!mbar_wait(wfull(it % C::WStages), (it / C::WStages) & 1, abort_flag, status)) {
+          if (!mbar_wait_warp(wfull(it % C::WStages), (it / C::WStages) & 1, abort_flag, status)) {
             ok = false;
             break;
           }
@@ -458,7 +447,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         ++seg;
         have = ok && prompt_work(p, blocks, seg, w);
         for (int r = 0; have && ok && r < 2; ++r) {
-          ok = mbar_wait(qfull(r), seg & 1, abort_flag, status) && (r == 1 || k_ready(it));
+          ok = mbar_wait_warp(qfull(r), seg & 1, abort_flag, status) && (r == 1 || k_ready(it));
           if (ok) {
             tc_fence_after_sync();
             scores(r, it);
@@ -757,8 +746,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     }
   };
-  if (warp == 1 && lane == 0) {
-    mma_commit(drain);
+  if (warp == 1) {
+    mma_commit_warp(drain);
     drain_wait(drain, 0);
   }
   if (warp == 0 && lane == 0 && *abort_flag) {
