@@ -16,8 +16,8 @@
 // The work is dealt out evenly, whatever the lengths: an item (request, head) weighs kItemUnits, what
 // its start and end cost, and one unit per 128-token tile; CTA c takes the tiles that lie in
 // [c U / G, (c + 1) U / G) of the flattened list (G = CTAs, at most U).  A CTA that holds part of an item
-// leaves its sums, maximum and unscaled output in the workspace, and k_attn_join adds the parts in CTA
-// order, so results do not depend on timing.
+// leaves its sums, maximum and unscaled output in the workspace; the CTA that arrives last adds the parts,
+// in CTA order, so results do not depend on timing.
 //   warp 0      producer: lane i fetches page i of the tile (TMA), its scales and the tile's bounds
 //   warp 1      MMA issuer
 //   warps 2..   one warpgroup per 16 rows: thread = token for the scores, = d for the output
@@ -67,7 +67,9 @@ struct FewSlot {
   int pos0, rows, q0, head;    // position of query token 0, live rows, row of it in q, key/value head
   int flags;                   // 2: last tile of the segment (the CTA's part of the item), 4: of the CTA
   int part;                    // workspace part that the segment fills, -1: the whole item is here
-  int pad[6];
+  int first_cta, parts;        // CTAs that share the item
+  int first_part;              // part of the first of them; the others' first segment has part 2 x CTA
+  int pad[3];
 };
 static_assert(sizeof(FewSlot) == 128, "slot");
 
@@ -76,8 +78,7 @@ struct FewParams {
   int G;                       // query heads per key/value head
   int page_shift;
   float* parts;                // [2 * gridDim.x][kNR * (kD + 2)]
-  int4* meta;                  // [gridDim.x] item that the CTA continues, item that it leaves open and
-                               // the part that holds it (-1: none)
+  int* arrived;                // [gridDim.x][4] per item that a CTA leaves open and 16 rows: parts done
   int* status;
 };
 
@@ -175,6 +176,76 @@ __device__ __forceinline__ uint64_t p_desc(uint32_t saddr) {
   return d;
 }
 
+// kRows rows of an item, from `row` on and below row1, out of its n parts: `first`, then 2 i after `rest`,
+// i = 1 .. n - 1.  One warp: the lanes read the parts' maxima and sums, then every lane its D / 32 values
+// of all rows, with as many loads under way as registers allow, for latency is all there is to it.
+template <int kD, int kNR, int kRows>
+__device__ __forceinline__ void join_rows(const FewParams& p, int first, int rest, int n, int row, int row1, int q0,
+                                          int head, int lane) {
+  constexpr size_t kPart = kNR * (kD + 2);
+  constexpr int kV = kD / 32;               // values of a row per lane
+  auto part = [&](int i) { return p.parts + (size_t)(i == 0 ? first : rest + 2 * i) * kPart; };
+  float m[kRows], l[kRows], acc[kRows][kV];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    m[r] = kNoScore;
+    l[r] = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) acc[r][v] = 0.0f;
+  }
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    // this group of parts: weights relative to the maximum so far
+    float w[kRows];
+    float2 ml[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      ml[r] = make_float2(kNoScore, 0.0f);
+      if (i0 + lane < n && row + r < row1)
+        ml[r] = __ldcg(reinterpret_cast<const float2*>(part(i0 + lane) + kNR * kD + 2 * (row + r)));
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      float top = fmaxf(m[r], ml[r].x);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+      const float alpha = m[r] == top ? 1.0f : exp2_approx(m[r] - top);
+      w[r] = ml[r].x == top ? 1.0f : exp2_approx(ml[r].x - top);
+      m[r] = top;
+      l[r] = __fmaf_rn(l[r], alpha, ml[r].y * w[r]);
+#pragma unroll
+      for (int v = 0; v < kV; ++v) acc[r][v] *= alpha;
+    }
+    const int k1 = min(32, n - i0);
+#pragma unroll(16 / kRows)
+    for (int k = 0; k < k1; ++k) {
+      const float* o = part(i0 + k) + lane * kV;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const float wk = __shfl_sync(~0u, w[r], k);
+        float x[kV];
+        const float* at = o + min(row + r, row1 - 1) * kD;
+        if (kV == 4) *reinterpret_cast<float4*>(x) = __ldcg(reinterpret_cast<const float4*>(at));
+        else *reinterpret_cast<float2*>(x) = __ldcg(reinterpret_cast<const float2*>(at));
+#pragma unroll
+        for (int v = 0; v < kV; ++v) acc[r][v] = __fmaf_rn(x[v], wk, acc[r][v]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) l[r] += __shfl_xor_sync(~0u, l[r], d);
+    if (row + r >= row1) break;
+    const float inv = l[r] > 0.0f || l[r] != l[r] ? 1.0f / l[r] : 0.0f;
+    const int i = (row + r) / p.G;
+    uint32_t* out = reinterpret_cast<uint32_t*>(
+        static_cast<uint16_t*>(p.a.out) + (int64_t)(q0 + i) * p.a.out_token_stride +
+        (int64_t)(head * p.G + row + r - i * p.G) * p.a.out_head_stride + lane * kV);
+    out[0] = pack_bf16x2(acc[r][0] * inv, acc[r][1] * inv);
+    if (kV == 4) out[1] = pack_bf16x2(acc[r][kV - 2] * inv, acc[r][kV - 1] * inv);
+  }
+}
+
 template <int kD, int kNR>
 __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::CtasPerSm)
     k_attn_few(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -197,11 +268,11 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
   auto sfull = [&](int b) { return bar0 + 8u * (kB + b); };
   const uint32_t qfull = bar0 + 8u * (kB + 2), pfull = bar0 + 8u * (kB + 3), ofull = bar0 + 8u * (kB + 4);
   const uint32_t drain = bar0 + 8u * (kB + 5);
-  static_assert(8 * (kB + 6) + 160 <= 1024, "barriers");
+  static_assert(8 * (kB + 6) + 16 + 208 <= 1024, "barriers");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (kB + 6));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* mma_done = reinterpret_cast<volatile int*>(tmem_slot + 2);
-  long long* scan = reinterpret_cast<long long*>(ctrl + 8 * (kB + 6) + 16);   // [warps + 2]
+  long long* scan = reinterpret_cast<long long*>(ctrl + 8 * (kB + 6) + 16);   // [warps + 2], an item
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* status = p.status;
@@ -242,7 +313,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
     if (lane >= d) pre += t;
   }
   constexpr int kWarps = C::Threads / 32;
-  static_assert(8 * (kWarps + 2) <= 160, "scan area");
+  static_assert(8 * (kWarps + 2) + (int)sizeof(FewItem) <= 208, "scan area");
   if (lane == 31) scan[warp] = pre;
   tc_fence_before_sync();
   __syncthreads();
@@ -256,15 +327,17 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
     total += scan[w];
   }
   // no more CTAs than units, so the CTAs that share an item are neighbours
-  const long long ctas = min((long long)gridDim.x, total), c = blockIdx.x;
+  const long long ctas = max(1ll, min((long long)gridDim.x, total)), c = blockIdx.x;
   const long long u0 = c < ctas ? total * c / ctas : 0, u1 = c < ctas ? total * (c + 1) / ctas : 0;
   if (u0 < u1 && u0 >= pre && u0 < pre + mine) {
     long long at = pre;
     for (int b = rb0; b < rb1; ++b) {
-      const long long w = weight(few_item<kNR>(p, b));
+      const FewItem it = few_item<kNR>(p, b);
+      const long long w = weight(it);
       if (u0 < at + w) {
         scan[kWarps] = b;
         scan[kWarps + 1] = u0 - at;
+        *reinterpret_cast<FewItem*>(scan + kWarps + 2) = it;
         break;
       }
       at += w;
@@ -278,7 +351,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
   cur.item = FewItem{};
   if (u0 < u1) {
     cur.b = (int)scan[kWarps];
-    cur.item = few_item<kNR>(p, cur.b);
+    cur.item = *reinterpret_cast<const FewItem*>(scan + kWarps + 2);
     const int u = (int)scan[kWarps + 1], per_item = cur.item.tiles + kItemUnits;
     cur.h = u / per_item;
     const int at = u - cur.h * per_item - kItemUnits;
@@ -297,12 +370,18 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       const int group = lane / npg, pi = lane - group * npg;
       const int batch = min(kBatch, 32 / npg);
       const bool leader = pi == 0;
-      const int first_item = cur.b * p.a.Hkv + cur.h;
-      const bool continues = cur.tile != 0;
+      // the CTA that has unit x
+      auto cta_of = [&](long long x) {
+        long long k = x * ctas / total;
+        while (total * (k + 1) / ctas <= x) ++k;
+        while (total * k / ctas > x) --k;
+        return (int)k;
+      };
       int seg = 0;
       struct Ahead {
         FewItem item;
-        int b, h, tile, page, part;      // page: -1 none; part: of the segment
+        int b, h, tile, page, seg;       // page: -1 none; seg: segments of the CTA before this one
+        int left;                        // units from the tile to the CTA's end
         int live;                        // 0: no such tile, 1: tile, 2: the CTA's last
       };
       // the lane's tile of the next batch, and its page
@@ -310,14 +389,15 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         Ahead a;
         a.live = 0;
         a.page = -1;
-        a.part = 0;
+        a.seg = a.left = 0;
         for (int k = 0; k < batch && cur.left > 0; ++k) {
           if (k == group) {
             a.item = cur.item;
             a.b = cur.b;
             a.h = cur.h;
             a.tile = cur.tile;
-            a.part = 2 * (int)blockIdx.x + (seg > 0 ? 1 : 0);
+            a.seg = seg;
+            a.left = (int)cur.left;
             a.live = 1;
           }
           if (cur.tile == cur.item.tiles - 1) ++seg;
@@ -338,15 +418,12 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           vs = p.a.v_scale[(size_t)a.page * p.a.Hkv + a.h];
         }
       };
-      int tail_item = -1, tail_part = -1;
-      Ahead now = look(), nxt = look();
+      Ahead now = look(), nxt;
       float ks, vs;
       scales(now, ks, vs);
       bool ok = true, more = true;
       for (int it = 0; ok && more;) {
-        const Ahead far = look();
-        float ks1, vs1;
-        scales(nxt, ks1, vs1);
+        const bool begins = it == 0;
         const bool live = now.page >= 0 && now.page < p.a.num_pages;
         const uint32_t pages = __ballot_sync(~0u, live);
         const uint32_t bytes = __popc((pages >> (group * npg)) & ((1u << npg) - 1)) * P * kD;
@@ -389,8 +466,6 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
             slot.vr[pi] = vr;
             if (leader) {
               const bool end = now.tile == now.item.tiles - 1, last = now.live == 2;
-              const int item = now.b * p.a.Hkv + now.h;
-              const bool continued = continues && item == first_item;
               slot.vref = vref;
               slot.token0 = (now.item.tile0 + now.tile) * kTile;
               slot.lo = now.item.lo;
@@ -400,11 +475,15 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
               slot.q0 = now.item.q0;
               slot.head = now.h;
               slot.flags = (end || last ? 2 : 0) | (last ? 4 : 0);
-              // an item that lies wholly in this CTA needs no part of the workspace
-              slot.part = end && !continued ? -1 : now.part;
-              if (last && !end && !continued) {
-                tail_item = item;
-                tail_part = now.part;
+              if (end || last) {
+                // the item's units: its own from `begin`, then its tiles
+                const long long begin = u1 - now.left - now.tile - kItemUnits;
+                const int first = cta_of(begin + kItemUnits);
+                const int n = cta_of(begin + kItemUnits + now.item.tiles - 1) - first + 1;
+                slot.part = n == 1 ? -1 : 2 * (int)blockIdx.x + (now.seg > 0 ? 1 : 0);
+                slot.first_cta = first;
+                slot.parts = n;
+                slot.first_part = 2 * first + (total * first / ctas < begin ? 1 : 0);
               }
             }
           }
@@ -414,16 +493,12 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           ++issued;
         }
         more = !__any_sync(~0u, now.live == 2);
+        if (begins) nxt = look();
+        const Ahead far = look();
+        scales(nxt, ks, vs);
         now = nxt;
         nxt = far;
-        ks = ks1;
-        vs = vs1;
       }
-      // the lane that met the CTA's last tile knows what it leaves open
-      tail_item = __reduce_max_sync(~0u, tail_item);
-      tail_part = __reduce_max_sync(~0u, tail_part);
-      const int head_item = continues ? first_item : -1;
-      if (lane == 0) p.meta[blockIdx.x] = make_int4(head_item, tail_item, tail_part, 0);
     } else if (warp == 1) {
       // ------------------------------------------------------------------------- MMA
       {
@@ -510,10 +585,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       };
       // Q of the segment that begins with tile `it`: 8 threads a row, D / 8 values each, two E4M3 terms.
       // The scores of the segment before are done: this warpgroup has read them.
-      auto load_q = [&](int it) {
-        const int s = it % C::Stages;
-        if (!mbar_wait(ifull(s), (it / C::Stages) & 1, abort_flag, status)) bad = true;
-        const int rows = bad ? 0 : slots[s].rows, q0 = slots[s].q0, head = slots[s].head;
+      auto load_q = [&](int rows, int q0, int head) {
         constexpr int kV = kD / 8;
         const int r = r0 + (wt >> 3), c = wt & 7;
         float x[kV];
@@ -568,7 +640,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         named_barrier_sync(1 + wg, 128);
         if (lane == 0) mbar_arrive(qfull);
       };
-      load_q(0);
+      load_q(cur.item.n * p.G, cur.item.q0, cur.h);   // the first segment's, before the producer has its pages
       for (int it = 0;; ++it) {
         const int s = it % C::Stages;
         if (!mbar_wait(ifull(s), (it / C::Stages) & 1, abort_flag, status)) bad = true;
@@ -684,7 +756,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         }
         vref_prev = slot.vref;
         pending = true;
-        const int part = slot.part;
+        const int part = slot.part, first_cta = slot.first_cta, parts = slot.parts, first_part = slot.first_part;
         const int flags = slot.flags;
         begin = flags & 2;
         fence_proxy_async_smem();
@@ -692,7 +764,11 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         if (lane == 0) mbar_arrive(pfull);
         if (begin) {
           // ------------------------------------------------------- end of the segment
-          if (!(flags & 4)) load_q(it + 1);    // while the last P V runs
+          if (!(flags & 4)) {                  // the next segment's, while the last P V runs
+            const int ns = (it + 1) % C::Stages;
+            if (!mbar_wait(ifull(ns), ((it + 1) / C::Stages) & 1, abort_flag, status)) bad = true;
+            load_q(bad ? 0 : slots[ns].rows, slots[ns].q0, slots[ns].head);
+          }
           add_output(it);
           pending = false;
           float lr[16], ar[16];
@@ -704,22 +780,51 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           const float sum = warp_reduce16<false>(lr, lane);
           if (!(lane & 1)) wred[q * 16 + (lane >> 1)] = sum;
           named_barrier_sync(1 + wg, 128);
+          // lane r and r + 16 know row r's sum and place; the others ask them
+          const int mr = lane & 15, my_row = r0 + mr;
+          const float lsum = (wred[mr] + wred[16 + mr]) + (wred[32 + mr] + wred[48 + mr]);
+          if (part < 0) {
+            const float inv = lsum > 0.0f || lsum != lsum ? 1.0f / lsum : 0.0f;
+            const int i = my_row / p.G;
+            const long long at = (long long)(q0 + i) * p.a.out_token_stride +
+                                 (long long)(head * p.G + my_row - i * p.G) * p.a.out_head_stride;
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const float lsum = (wred[r] + wred[16 + r]) + (wred[32 + r] + wred[48 + r]);
-            const int row = r0 + r;
-            if (row >= rows || !holds_d) continue;
-            if (part < 0) {
-              const int i = row / p.G;
-              static_cast<uint16_t*>(p.a.out)[(int64_t)(q0 + i) * p.a.out_token_stride +
-                                              (int64_t)(head * p.G + row - i * p.G) * p.a.out_head_stride + d] =
-                  (uint16_t)f32_to_bf16_bits(lsum > 0.0f || lsum != lsum ? ar[r] / lsum : 0.0f);
-            } else {
-              float* o = p.parts + (size_t)part * (kNR * (kD + 2));
-              o[row * kD + d] = ar[r];
-              if (d == 0) {
-                o[kNR * kD + 2 * row] = m[r];
-                o[kNR * kD + 2 * row + 1] = lsum;
+            for (int r = 0; r < 16; ++r) {
+              if (r0 + r >= rows) break;
+              const float f = __shfl_sync(~0u, inv, r);
+              const long long o = __shfl_sync(~0u, at, r);
+              if (holds_d) static_cast<uint16_t*>(p.a.out)[o + d] = (uint16_t)f32_to_bf16_bits(ar[r] * f);
+            }
+          } else {
+            float* o = p.parts + (size_t)part * (kNR * (kD + 2));
+            float mm = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              if (mr == r) mm = m[r];
+              if (r0 + r < rows && holds_d) o[(r0 + r) * kD + d] = ar[r];
+            }
+            if (wt < 16 && my_row < rows)
+              *reinterpret_cast<float2*>(o + kNR * kD + 2 * my_row) = make_float2(mm, lsum);
+          }
+          if (part >= 0) {
+            // the last of the item's CTAs to get here adds the parts
+            __threadfence();
+            named_barrier_sync(1 + wg, 128);
+            int* arrived = p.arrived + 4 * first_cta + wg;
+            if (wt == 0) {
+              const int before = atomicAdd(arrived, 1);
+              if (before == parts - 1) *arrived = 0;
+              __threadfence();
+              wred[0] = before == parts - 1 ? 1.0f : 0.0f;
+            }
+            named_barrier_sync(1 + wg, 128);
+            if (wred[0] != 0.0f) {
+              const int row1 = min(rows, r0 + 16), jw = wt >> 5;
+              if (kNR == 64 || row1 - r0 <= 4) {     // 64 rows: no registers for four at once
+                for (int row = r0 + jw; row < row1; row += 4)
+                  join_rows<kD, kNR, 1>(p, first_part, 2 * first_cta, parts, row, row1, q0, head, lane);
+              } else if (r0 + 4 * jw < row1) {
+                join_rows<kD, kNR, 4>(p, first_part, 2 * first_cta, parts, r0 + 4 * jw, row1, q0, head, lane);
               }
             }
           }
@@ -728,8 +833,6 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         }
       }
     }
-  } else if (threadIdx.x == 0) {
-    p.meta[blockIdx.x] = make_int4(-1, -1, -1, 0);
   }
 
   // ------------------------------------------------------------------------ teardown
@@ -762,78 +865,6 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
   }
 }
 
-// Joins the parts of an item that several CTAs hold.  Block c looks after the item that CTA c leaves
-// open (if any): CTA c's last segment, then the first segments of the CTAs that continue it.
-// blockIdx.y: rows, one after another.  The parts' weights are formed by all threads at once and the
-// outputs added with several loads under way, since latency is all there is to it.
-template <int kD, int kNR>
-__global__ void __launch_bounds__(kD) k_attn_join(const FewParams p, int ctas) {
-  __shared__ float wgt[304], red[kD / 32], red2[kD / 32];
-  grid_dep_wait();
-  const int c = blockIdx.x, tid = threadIdx.x;
-  const int4 me = p.meta[c];
-  if (me.y < 0) return;
-  const int b = me.y / p.a.Hkv, h = me.y - b * p.a.Hkv;
-  const int q0 = p.a.tok_start[b], rows = (p.a.tok_start[b + 1] - q0) * p.G;
-  // parts: this CTA's last segment, then those of CTAs c + 1 .. c + n - 1
-  int n = 1;
-  for (int base = c + 1; base < ctas; base += kD) {
-    const int at = base + tid;
-    const int got = __syncthreads_count(at < ctas && p.meta[at].x == me.y);
-    n += got;
-    if (got < kD) break;
-  }
-  constexpr size_t kPart = kNR * (kD + 2);
-  const float* part0 = p.parts + (size_t)me.z * kPart;
-  const float* rest = p.parts + (size_t)(2 * c) * kPart;     // part i >= 1 is 2 (c + i)
-  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-    constexpr int kMine = (304 + kD - 1) / kD;
-    float mi[kMine], li[kMine], m = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      const int i = tid + k * kD;
-      mi[k] = -INFINITY;
-      li[k] = 0.0f;
-      if (i < n) {
-        const float* o = (i == 0 ? part0 : rest + 2 * i * kPart) + kNR * kD + 2 * row;
-        mi[k] = o[0];
-        li[k] = o[1];
-      }
-      m = fmaxf(m, mi[k]);
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-    if ((tid & 31) == 0) red[tid >> 5] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kD / 32; ++w) m = fmaxf(m, red[w]);
-    float l = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      const int i = tid + k * kD;
-      const float w = mi[k] == m ? 1.0f : exp2_approx(mi[k] - m);
-      if (i < n) wgt[i] = w;
-      l = __fmaf_rn(li[k], w, l);
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-    if ((tid & 31) == 0) red2[tid >> 5] = l;
-    __syncthreads();
-    l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kD / 32; ++w) l += red2[w];
-    float acc = part0[row * kD + tid] * wgt[0];
-    const float* o = rest + row * kD + tid;
-#pragma unroll 8
-    for (int i = 1; i < n; ++i) acc = __fmaf_rn(o[2 * i * kPart], wgt[i], acc);
-    const int i = row / p.G;
-    static_cast<uint16_t*>(p.a.out)[(int64_t)(q0 + i) * p.a.out_token_stride +
-                                    (int64_t)(h * p.G + row - i * p.G) * p.a.out_head_stride + tid] =
-        (uint16_t)f32_to_bf16_bits(l > 0.0f || l != l ? acc / l : 0.0f);
-    __syncthreads();
-  }
-}
-
 // ------------------------------------------------------------------------------------ launch
 // Rows per item of a call: tokens of a request x heads that share a key/value head, 16, 32 or 64.
 int few_rows(int G, int max_q) {
@@ -846,7 +877,7 @@ static int few_ctas(int nr) { return nr == 16 ? 304 : 152; }   // at most; 152 S
 
 size_t few_workspace_bytes(int D, int nr) {
   const int ctas = few_ctas(nr);
-  return 256 + (size_t)ctas * sizeof(int4) + (size_t)2 * ctas * nr * (D + 2) * 4;
+  return 256 + (size_t)ctas * 16 + (size_t)2 * ctas * nr * (D + 2) * 4;
 }
 
 template <int kD, int kNR>
@@ -866,12 +897,9 @@ static cudaError_t launch(const moe_kv_attention_args& a, void* workspace, cudaS
   p.page_shift = __builtin_ctz((unsigned)a.page_size);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.status = reinterpret_cast<int*>(ws);
-  p.meta = reinterpret_cast<int4*>(ws + 256);
-  p.parts = reinterpret_cast<float*>(ws + 256 + (size_t)few_ctas(kNR) * sizeof(int4));
-  err = launch_pdl(k_attn_few<kD, kNR>, dim3(ctas), dim3(C::Threads), C::Smem, s, tmK, tmV, p);
-  if (err != cudaSuccess) return err;
-  const int rows = std::min<long long>((long long)p.G * a.max_q, kNR);
-  return launch_pdl(k_attn_join<kD, kNR>, dim3(ctas, std::min(rows, 8)), dim3(kD), 0, s, p, ctas);
+  p.arrived = reinterpret_cast<int*>(ws + 256);
+  p.parts = reinterpret_cast<float*>(ws + 256 + (size_t)few_ctas(kNR) * 16);
+  return launch_pdl(k_attn_few<kD, kNR>, dim3(ctas), dim3(C::Threads), C::Smem, s, tmK, tmV, p);
 }
 
 cudaError_t launch_attn_few(const moe_kv_attention_args& a, int nr, void* workspace, cudaStream_t s) {
