@@ -109,18 +109,20 @@ __device__ __forceinline__ uint64_t rows_desc(uint32_t saddr) {
   return d;
 }
 
-// The cache's codes as (value, row of the page, head, page); one box is a page of one head, laid out
-// in rows of D bytes with the swizzle of that width.
-inline bool cache_map(CUtensorMap* m, const void* codes, int D, int P, int Hkv, int pages) {
+// The cache's codes as (value, row of the page, head, page); a box is box_rows rows of one page and head
+// and box_d of its values, laid out in rows of box_d bytes: with the swizzle of that width when it is a
+// whole head, else as they come.
+inline bool cache_map(CUtensorMap* m, const void* codes, int D, int P, int Hkv, int pages, int box_rows, int box_d) {
   const EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)P, (cuuint64_t)Hkv, (cuuint64_t)pages};
   const cuuint64_t strides[3] = {(cuuint64_t)D, (cuuint64_t)P * D, (cuuint64_t)Hkv * P * D};
-  const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)P, 1, 1};
+  const cuuint32_t box[4] = {(cuuint32_t)box_d, (cuuint32_t)box_rows, 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(codes), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE,
-            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            box_d < D ? CU_TENSOR_MAP_SWIZZLE_NONE
+                      : D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

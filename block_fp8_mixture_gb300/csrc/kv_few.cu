@@ -50,6 +50,7 @@ struct FewCfg {
   static constexpr int SCols = 2 * kNR;                     // per score buffer, two of them
   static constexpr int OCol = 2 * SCols;
   static constexpr int TmemCols = kNR == 16 ? 128 : kNR == 32 ? 256 : 512;
+  static constexpr int LdCols = kNR == 64 ? 8 : 16;         // 64 rows: 96 registers a thread
   static constexpr int SlotBytes = 128;
   static constexpr int CtrlBytes = 1024 + Stages * SlotBytes + WGs * 5 * 16 * 4;
   static constexpr int Smem = 1024 + Stages * StageBytes + QBytes + PBytes + CtrlBytes;
@@ -149,6 +150,20 @@ __device__ __forceinline__ float warp_reduce16(float (&v)[16], int lane) {
   }
   const float got = __shfl_xor_sync(~0u, v[0], 1);
   return kMax ? fmaxf(v[0], got) : v[0] + got;
+}
+
+// kN consecutive 32-bit tensor-memory columns of this warp's lanes (8 or 16).
+template <int kN>
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[kN]) {
+  if constexpr (kN == 16) {
+    tmem_ld16(taddr, r);
+  } else {
+    static_assert(kN == 8, "8 or 16 columns");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+  }
 }
 
 // Two FP16 values -> the E4M3 codes nearest to them, and 32 x what those leave over (exact in FP16:
@@ -568,19 +583,23 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           return;
         }
         tc_fence_after_sync();
-        uint32_t t[3][16];
-        const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + C::OCol + r0;
-#pragma unroll
-        for (int k = 0; k < 3; ++k) tmem_ld16(at + k * kNR, t[k]);
-        tmem_ld_wait();
         const float f = vref_prev * (1.0f / kPScale);
         const f32x2 f2 = pack2(f, f), step = pack2(1.0f / kTermStep, 1.0f / kTermStep);
-        auto pair = [&](int k, int r) {
-          return pack2(__uint_as_float(t[k][2 * r]), __uint_as_float(t[k][2 * r + 1]));
-        };
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          acc[r] = fma2(fma2(fma2(pair(2, r), step, pair(1, r)), step, pair(0, r)), f2, acc[r]);
+        for (int r0s = 0; r0s < 16; r0s += C::LdCols) {
+          uint32_t t[3][C::LdCols];
+          const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + C::OCol + r0 + r0s;
+#pragma unroll
+          for (int k = 0; k < 3; ++k) tmem_ldn<C::LdCols>(at + k * kNR, t[k]);
+          tmem_ld_wait();
+          auto pair = [&](int k, int r) {
+            return pack2(__uint_as_float(t[k][2 * r]), __uint_as_float(t[k][2 * r + 1]));
+          };
+#pragma unroll
+          for (int r = 0; r < C::LdCols / 2; ++r)
+            acc[r0s / 2 + r] =
+                fma2(fma2(fma2(pair(2, r), step, pair(1, r)), step, pair(0, r)), f2, acc[r0s / 2 + r]);
+        }
         tc_fence_before_sync();
       };
       // Q of the segment that begins with tile `it`: 8 threads a row, D / 8 values each, two E4M3 terms.
@@ -669,25 +688,28 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         tc_fence_after_sync();
         float sc[16];
         {
-          uint32_t t[16], t2[16];
-          const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (it & 1) * C::SCols + r0;
-          tmem_ld16(at, t);
-          tmem_ld16(at + kNR, t2);
-          tmem_ld_wait();
-          tc_fence_before_sync();
           const f32x2 step = pack2(1.0f / kTermStep, 1.0f / kTermStep), kf2 = pack2(kf, kf);
 #pragma unroll
-          for (int r = 0; r < 16; r += 4) {
-            const float4 qs = *reinterpret_cast<const float4*>(wqs + r);
+          for (int r0s = 0; r0s < 16; r0s += C::LdCols) {
+            uint32_t t[C::LdCols], t2[C::LdCols];
+            const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (it & 1) * C::SCols + r0 + r0s;
+            tmem_ldn<C::LdCols>(at, t);
+            tmem_ldn<C::LdCols>(at + kNR, t2);
+            tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int x = r + 2 * i;
-              const f32x2 v = fma2(pack2(__uint_as_float(t2[x]), __uint_as_float(t2[x + 1])), step,
-                                   pack2(__uint_as_float(t[x]), __uint_as_float(t[x + 1])));
-              const f32x2 f = mul2(i ? pack2(qs.z, qs.w) : pack2(qs.x, qs.y), kf2);
-              unpack2(mul2(v, f), sc[x], sc[x + 1]);
+            for (int r = 0; r < C::LdCols; r += 4) {
+              const float4 qs = *reinterpret_cast<const float4*>(wqs + r0s + r);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int x = r + 2 * i;
+                const f32x2 v = fma2(pack2(__uint_as_float(t2[x]), __uint_as_float(t2[x + 1])), step,
+                                     pack2(__uint_as_float(t[x]), __uint_as_float(t[x + 1])));
+                const f32x2 f = mul2(i ? pack2(qs.z, qs.w) : pack2(qs.x, qs.y), kf2);
+                unpack2(mul2(v, f), sc[r0s + x], sc[r0s + x + 1]);
+              }
             }
           }
+          tc_fence_before_sync();
           if (seen != 0xFFFFu) {
 #pragma unroll
             for (int r = 0; r < 16; ++r)
@@ -884,8 +906,8 @@ template <int kD, int kNR>
 static cudaError_t launch(const moe_kv_attention_args& a, void* workspace, cudaStream_t s) {
   using C = FewCfg<kD, kNR>;
   CUtensorMap tmK, tmV;
-  if (!cache_map(&tmK, a.k_codes, kD, a.page_size, a.Hkv, a.num_pages) ||
-      !cache_map(&tmV, a.v_codes, kD, a.page_size, a.Hkv, a.num_pages))
+  if (!cache_map(&tmK, a.k_codes, kD, a.page_size, a.Hkv, a.num_pages, a.page_size, kD) ||
+      !cache_map(&tmV, a.v_codes, kD, a.page_size, a.Hkv, a.num_pages, a.page_size, kD))
     return cudaErrorInvalidValue;
   cudaError_t err = cudaFuncSetAttribute(k_attn_few<kD, kNR>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem);

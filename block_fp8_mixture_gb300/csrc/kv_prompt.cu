@@ -28,7 +28,8 @@
 
 namespace moe {
 
-constexpr int kBlockRows = 256;
+constexpr int kBlockRows = 512;              // of a pair of CTAs
+constexpr int kCtaRows = 256;
 constexpr int kPromptThreads = 512;
 constexpr int kPromptCtas = 152;              // at most (SMs)
 constexpr int kMaxBlocks = 1 << 16;           // blocks of a call, without the heads
@@ -44,12 +45,13 @@ template <int kD>
 struct PromptCfg {
   static constexpr int QTerm = 128 * kD;                 // one E4M3 term of a row tile
   static constexpr int QBytes = 4 * QTerm;               // [row tile][term]
-  static constexpr int Half = kTile * kD;                // K or V codes of a tile
-  static constexpr int KStages = 3, VStages = 2, WStages = 2, Slots = 4;
-  static constexpr int WBytes = kTile * kD * 2;          // V of a tile in FP16
-  static constexpr int Tiles = QBytes + KStages * Half + VStages * Half + WStages * WBytes;
+  static constexpr int KBytes = kTile / 2 * kD;          // K codes: this CTA's half of the tokens
+  static constexpr int VBytes = kTile * kD / 2;          // V codes: this CTA's half of the values
+  static constexpr int WBytes = 2 * VBytes;              // the same in FP16
+  static constexpr int KStages = 4, VStages = 3, WStages = 3, Slots = 6;
+  static constexpr int Tiles = QBytes + KStages * KBytes + VStages * VBytes + WStages * WBytes;
   static constexpr int Smem = 1024 + Tiles + 1024 + Slots * 128;
-  static constexpr int PartFloats = kBlockRows * (kD + 2);
+  static constexpr int PartFloats = kCtaRows * (kD + 2);
   static_assert(Smem <= 232448, "shared memory");
 };
 
@@ -65,11 +67,11 @@ struct PromptParams {
   int2* list;                  // blocks (request, block), longest first
   int* bins;                   // scratch of the order
   int* count;                  // blocks
-  float* parts;                // [gridDim.x][PartFloats]
+  float* parts;                // [CTA][PartFloats]
   int* status;
 };
 
-// One block's rows and the tokens that they see; tiles [t0, t1) of it for this CTA.
+// One block's rows and the tokens that they see; tiles [t0, t1) of it for this pair of CTAs.
 struct PromptWork {
   int b, h, row0, rows, q0, pos0, lo, hi, t0, t1;
   int part;                    // workspace part, -1: the whole block is here
@@ -90,9 +92,9 @@ __device__ __forceinline__ void prompt_block(const PromptParams& p, int b, int b
   w.t1 = max(w.t0 + 1, (w.hi + kTile - 1) / kTile);
 }
 
-// The k-th piece of work of this CTA; false when there is none.
+// The k-th piece of work of this pair of CTAs; false when there is none.
 __device__ __forceinline__ bool prompt_work(const PromptParams& p, int blocks, int k, PromptWork& w) {
-  const int C = gridDim.x, c = blockIdx.x;
+  const int C = gridDim.x / 2, c = blockIdx.x / 2;
   const int items = blocks * p.a.Hkv, rounds = items / C, rest = items - rounds * C;
   int item, piece = 0, pieces = 1;
   if (k < rounds) {
@@ -116,7 +118,7 @@ __device__ __forceinline__ bool prompt_work(const PromptParams& p, int blocks, i
     const int t0 = w.t0;
     w.t0 = t0 + nt * piece / np;
     w.t1 = t0 + nt * (piece + 1) / np;
-    if (np > 1) w.part = c;
+    if (np > 1) w.part = blockIdx.x;
   }
   return true;
 }
@@ -228,6 +230,83 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// ------------------------------------------------------------------------------ pairs of CTAs
+// Two CTAs of a cluster, on neighbouring SMs, run one product of 256 rows: each holds its 128 rows of A
+// and of the result and half of B, so that B, which bounds shared memory's bandwidth when one CTA does it
+// alone, is read and laid out once for both.  The leader (rank 0) issues; its peer's warps arrive on the
+// leader's barriers, and commits arrive on both CTAs'.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Arrive on the leader's barrier at this offset.  What the arrival announces is read by the tensor core
+// of the arriving thread's own SM, behind the proxy or tcgen05 fence that came before, not by the
+// leader's threads, so the arrival needs no cluster-wide release (which costs 1.4x the whole kernel).
+__device__ __forceinline__ void mbar_arrive_leader(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
+      : "memory");
+}
+
+// mbar_wait_warp for barriers that the peer arrives on: the phase's writes are acquired cluster-wide.
+__device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                               int* status) {
+  auto done = [&] {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return r != 0;
+  };
+  bool ok = done();
+  if (!ok) ok = mbar_wait(bar, parity, abort_flag, status) && done();
+  return __all_sync(~0u, ok);
+}
+
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+__device__ __forceinline__ void pair_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(KV_ELECT "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+               : "memory");
+}
+
+__device__ __forceinline__ void pair_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(KV_ELECT "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+               "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+               : "memory");
+}
+
+// Arrive on both CTAs' barrier at this offset when the elected lane's products so far are complete.
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::
+          "r"(bar), "h"((uint16_t)3)
+      : "memory");
+}
+
 template <int kRegs>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -246,25 +325,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - raw);
-  const uint32_t sQ = sbase, sK = sQ + C::QBytes, sV = sK + C::KStages * C::Half,
-                 sW = sV + C::VStages * C::Half;
+  const uint32_t sQ = sbase, sK = sQ + C::QBytes, sV = sK + C::KStages * C::KBytes,
+                 sW = sV + C::VStages * C::VBytes;
   uint8_t* ctrl = smem + C::Tiles;
   PromptSlot* slots = reinterpret_cast<PromptSlot*>(ctrl + 1024);
   const uint32_t bar0 = smem_addr(ctrl);
+  const int rank = (int)cluster_rank();
   auto kfull = [&](int s) { return bar0 + 8u * s; };
-  auto kempty = [&](int s) { return bar0 + 8u * (4 + s); };
-  auto vfull = [&](int s) { return bar0 + 8u * (8 + s); };
-  auto vempty = [&](int s) { return bar0 + 8u * (12 + s); };
-  auto wfull = [&](int s) { return bar0 + 8u * (16 + s); };
-  auto wempty = [&](int s) { return bar0 + 8u * (20 + s); };
-  auto ifull = [&](int s) { return bar0 + 8u * (24 + s); };
-  auto iempty = [&](int s) { return bar0 + 8u * (28 + s); };
-  auto qfull = [&](int w) { return bar0 + 8u * (32 + w); };
-  auto sfull = [&](int w) { return bar0 + 8u * (34 + w); };
-  auto pfull = [&](int w, int half) { return bar0 + 8u * (36 + 2 * w + half); };
-  auto ofull = [&](int w) { return bar0 + 8u * (40 + w); };
-  const uint32_t drain = bar0 + 8u * 42;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * 43);
+  auto kempty = [&](int s) { return bar0 + 8u * (8 + s); };
+  auto vfull = [&](int s) { return bar0 + 8u * (16 + s); };
+  auto vempty = [&](int s) { return bar0 + 8u * (24 + s); };
+  auto wempty = [&](int s) { return bar0 + 8u * (32 + s); };
+  auto ifull = [&](int s) { return bar0 + 8u * (40 + s); };
+  auto iempty = [&](int s) { return bar0 + 8u * (48 + s); };
+  auto sfull = [&](int w) { return bar0 + 8u * (56 + w); };
+  auto ofull = [&](int w) { return bar0 + 8u * (58 + w); };
+  // the leader's: the peer's K has landed, V in FP16, Q and P of both CTAs
+  auto kpeer = [&](int s) { return bar0 + 8u * (60 + s); };
+  auto wfull = [&](int s) { return bar0 + 8u * (68 + s); };
+  auto qfull = [&](int w) { return bar0 + 8u * (76 + w); };
+  auto pfull = [&](int w, int half) { return bar0 + 8u * (78 + 2 * w + half); };
+  const uint32_t drain = bar0 + 8u * 82;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * 83);
+  static_assert(8 * 83 + 16 <= 1024 && C::KStages <= 8 && C::Slots <= 8, "barriers");
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* k_done = reinterpret_cast<volatile int*>(tmem_slot + 2);
   volatile int* v_done = reinterpret_cast<volatile int*>(tmem_slot + 3);
@@ -272,22 +355,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* status = p.status;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < 8; ++s) {
       mbar_init(kfull(s), 1);
       mbar_init(kempty(s), 1);
       mbar_init(vfull(s), 1);
       mbar_init(vempty(s), 4);
-      mbar_init(wfull(s), 4);
       mbar_init(wempty(s), 1);
       mbar_init(ifull(s), 1);
       mbar_init(iempty(s), 8);
+      mbar_init(kpeer(s), 1);
+      mbar_init(wfull(s), 8);
     }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(qfull(w), 4);
       mbar_init(sfull(w), 1);
-      mbar_init(pfull(w, 0), 4);
-      mbar_init(pfull(w, 1), 4);
       mbar_init(ofull(w), 1);
+      mbar_init(qfull(w), 8);
+      mbar_init(pfull(w, 0), 8);
+      mbar_init(pfull(w, 1), 8);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -297,9 +381,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
   }
-  if (warp == 1) tmem_alloc(smem_addr(tmem_slot), 512);
+  if (warp == 1) pair_tmem_alloc(smem_addr(tmem_slot), 512);
   tc_fence_before_sync();
   __syncthreads();
+  cluster_sync();                  // both CTAs' barriers are there
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   grid_dep_wait();
@@ -312,6 +397,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     if (warp == 0) {
       // -------------------------------------------------------------------- producer
       const int npg = kTile >> p.page_shift, P = 1 << p.page_shift;
+      // K: this CTA's 64 tokens, in boxes of a page or half of one
+      const int krows = min(P, kTile / 2), kboxes = kTile / 2 / krows;
       bool ok = true;
       int it = 0;
       PromptWork w;
@@ -338,11 +425,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                  mbar_wait(kempty(sk), ((it / C::KStages) & 1) ^ 1, abort_flag, status);
           ok = __shfl_sync(~0u, (int)ok, 0);
           if (!ok) break;
-          const uint32_t bytes = __popc(__ballot_sync(~0u, page >= 0)) * P * kD;
-          if (lane == 0) mbar_arrive_expect_tx(kfull(sk), bytes);
+          // lane i: box i of K
+          const int kpage = __shfl_sync(~0u, page, P == kTile ? 0 : (rank * kboxes + lane) & 31);
+          const bool klive = lane < kboxes && kpage >= 0;
+          const uint32_t kbytes = __popc(__ballot_sync(~0u, klive)) * krows * kD;
+          if (lane == 0) mbar_arrive_expect_tx(kfull(sk), kbytes);
           __syncwarp();
-          if (page >= 0)
-            tma_load_4d(sK + sk * C::Half + lane * P * kD, &tmK, 0, 0, w.h, page, kfull(sk));
+          if (klive)
+            tma_load_4d(sK + sk * C::KBytes + lane * krows * kD, &tmK, 0, P == kTile ? rank * krows : 0, w.h,
+                        kpage, kfull(sk));
           if (lane == 0) *k_done = it + 1;      // copies issued so far
           // scales of the tile's groups of 16 tokens
           const int src = (lane * 16) >> p.page_shift;
@@ -360,10 +451,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           ok = __shfl_sync(~0u, (int)ok, 0);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(vfull(sv), bytes);
+          const uint32_t vbytes = __popc(__ballot_sync(~0u, page >= 0)) * P * (kD / 2);
+          if (lane == 0) mbar_arrive_expect_tx(vfull(sv), vbytes);
           __syncwarp();
           if (page >= 0)
-            tma_load_4d(sV + sv * C::Half + lane * P * kD, &tmV, 0, 0, w.h, page, vfull(sv));
+            tma_load_4d(sV + sv * C::VBytes + lane * P * (kD / 2), &tmV, rank * (kD / 2), 0, w.h, page, vfull(sv));
           if (lane == 0) *v_done = it + 1;
           page = page1;
           page1 = page2;
@@ -371,58 +463,66 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           vs = vs1;
         }
       }
+    } else if (warp == 1 && rank == 1) {
+      // ------------------------------------------------- the peer's K has landed: tell the leader
+      bool ok = true;
+      int it = 0;
+      PromptWork w;
+      for (int k = 0; ok && prompt_work(p, blocks, k, w); ++k) {
+        for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
+          ok = mbar_wait_warp(kfull(it % C::KStages), (it / C::KStages) & 1, abort_flag, status);
+          if (ok && lane == 0) mbar_arrive_leader(kpeer(it % C::KStages));
+        }
+      }
     } else if (warp == 1) {
       // ------------------------------------------------------------------------- MMA
-      constexpr uint32_t kIdescS = make_idesc_e4m3(128, kTile);
-      // D fp32, A and B FP16, B MN-major, 128 x kD
-      constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(kD >> 3) << 17) | (8u << 24);
+      constexpr uint32_t kIdescS = make_idesc_e4m3(256, kTile);
+      // D fp32, A and B FP16, B MN-major, 256 x kD
+      constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(kD >> 3) << 17) | (16u << 24);
       bool ok = true;
       int it = 0, seg = 0;                   // tiles whose P V has been issued, pieces begun
       // S of row tile w for tile `tile`
       auto scores = [&](int w, int tile) {
-        const uint64_t kd = rows_desc<kD>(sK + tile % C::KStages * C::Half);
+        const uint64_t kd = rows_desc<kD>(sK + tile % C::KStages * C::KBytes);
 #pragma unroll
         for (int term = 0; term < 2; ++term) {
           const uint64_t qd = rows_desc<kD>(sQ + (2 * w + term) * C::QTerm);
 #pragma unroll
           for (int k = 0; k < kD / 32; ++k)
-            mma_f8_warp(tmem + 128 * w, qd + 2 * k, kd + 2 * k, kIdescS, term + k > 0);
+            pair_mma_f8(tmem + 128 * w, qd + 2 * k, kd + 2 * k, kIdescS, term + k > 0);
         }
-        mma_commit_warp(sfull(w));
-        if (w == 1) mma_commit_warp(kempty(tile % C::KStages));
+        pair_commit(sfull(w));
+        if (w == 1) pair_commit(kempty(tile % C::KStages));
       };
       auto k_ready = [&](int tile) {
-        return mbar_wait_warp(kfull(tile % C::KStages), (tile / C::KStages) & 1, abort_flag, status);
+        const int s = tile % C::KStages, ph = (tile / C::KStages) & 1;
+        return mbar_wait_warp(kfull(s), ph, abort_flag, status) && mbar_wait_pair(kpeer(s), ph, abort_flag, status);
       };
       // P arrives in two halves of the tile's tokens: the product of the first runs while the softmax
       // warps form the second
       auto output = [&](int w, int tile, bool first) {
-        const uint32_t wt = sW + tile % C::WStages * C::WBytes;
-        // V in FP16: rows of 64 values (128 bytes), the second half of the values 16 KB further
-        uint64_t vd = make_sdesc_sw128(wt, 1024);
-        vd = (vd & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)((kTile * 128) >> 4) << 16);
+        const uint64_t vd = rows_desc<kD>(sW + tile % C::WStages * C::WBytes);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!mbar_wait_warp(pfull(w, half), tile & 1, abort_flag, status)) return false;
+          if (!mbar_wait_pair(pfull(w, half), tile & 1, abort_flag, status)) return false;
           tc_fence_after_sync();
 #pragma unroll
           for (int k = 4 * half; k < 4 * half + 4; ++k)
-            mma_f16_ts_warp(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, vd + k * (16 * 128 / 16), kIdescO,
-                       !first || k > 0);
+            pair_mma_f16_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, vd + k * kD, kIdescO, !first || k > 0);
         }
-        mma_commit_warp(ofull(w));
-        if (w == 1) mma_commit_warp(wempty(tile % C::WStages));
+        pair_commit(ofull(w));
+        if (w == 1) pair_commit(wempty(tile % C::WStages));
         return true;
       };
       PromptWork w;
       bool have = prompt_work(p, blocks, 0, w);
       if (have) {
-        ok = mbar_wait_warp(qfull(0), 0, abort_flag, status) && k_ready(0);
+        ok = mbar_wait_pair(qfull(0), 0, abort_flag, status) && k_ready(0);
         if (ok) {
           tc_fence_after_sync();
           scores(0, 0);
         }
-        ok = ok && mbar_wait_warp(qfull(1), 0, abort_flag, status);
+        ok = ok && mbar_wait_pair(qfull(1), 0, abort_flag, status);
         if (ok) {
           tc_fence_after_sync();
           scores(1, 0);
@@ -431,7 +531,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       while (ok && have) {
         const int nt = w.t1 - w.t0;
         for (int t = 0; ok && t < nt; ++t, ++it) {
-          if (!mbar_wait_warp(wfull(it % C::WStages), (it / C::WStages) & 1, abort_flag, status)) {
+          if (!mbar_wait_pair(wfull(it % C::WStages), (it / C::WStages) & 1, abort_flag, status)) {
             ok = false;
             break;
           }
@@ -447,7 +547,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         ++seg;
         have = ok && prompt_work(p, blocks, seg, w);
         for (int r = 0; have && ok && r < 2; ++r) {
-          ok = mbar_wait_warp(qfull(r), seg & 1, abort_flag, status) && (r == 1 || k_ready(it));
+          ok = mbar_wait_pair(qfull(r), seg & 1, abort_flag, status) && (r == 1 || k_ready(it));
           if (ok) {
             tc_fence_after_sync();
             scores(r, it);
@@ -458,7 +558,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   } else if (warp < 8) {
     // ------------------------------------------------------------------------ V codes -> FP16
     regs_down<kRegsWiden>();
-    constexpr int kChunks = kD / 16;         // 16 codes each
+    constexpr int kChunks = kD / 32;         // 16 codes each; rows of kD / 2 codes
     constexpr int kRowsAt = 32 / kChunks;    // rows of a warp's load
     const int c = lane % kChunks, rl = lane / kChunks;
     bool ok = true;
@@ -471,14 +571,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
              mbar_wait(wempty(sw), ((it / C::WStages) & 1) ^ 1, abort_flag, status);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
-        const uint8_t* in = smem + (sV - sbase) + sv * C::Half;
+        const uint8_t* in = smem + (sV - sbase) + sv * C::VBytes;
         uint8_t* out = smem + (sW - sbase) + sw * C::WBytes;
         const int token0 = t * kTile;
         const bool edge = token0 < w.lo || token0 + kTile > w.hi;
 #pragma unroll 4
         for (int i = 0; i < 32 / kRowsAt; ++i) {
           const int r = (warp & 3) * 32 + i * kRowsAt + rl;
-          uint4 x = *reinterpret_cast<const uint4*>(in + swz<kD>(r, 16 * c));
+          uint4 x = *reinterpret_cast<const uint4*>(in + r * (kD / 2) + 16 * c);
           // rows that no query row sees may hold anything: 0 x NaN would spread
           if (edge && (token0 + r < w.lo || token0 + r >= w.hi)) x = make_uint4(0, 0, 0, 0);
           const uint32_t u[4] = {x.x, x.y, x.z, x.w};
@@ -488,20 +588,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * j]) : "h"((uint16_t)u[j]));
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * j + 1]) : "h"((uint16_t)(u[j] >> 16)));
           }
-          // lanes of the two halves store their 16-byte pieces in opposite order: no bank conflicts
-          const int half = c >> 2, col = (c & 3) * 32;
-          uint8_t* o = out + half * (kTile * 128);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int piece = e ^ half;
-            *reinterpret_cast<uint4*>(o + swz<128>(r, col + 16 * piece)) =
-                piece ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
-          }
+          *reinterpret_cast<uint4*>(out + swz<kD>(r, 32 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(out + swz<kD>(r, 32 * c + 16)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(wfull(sw));
+          mbar_arrive_leader(wfull(sw));
           mbar_arrive(vempty(sv));
         }
       }
@@ -517,7 +610,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
     // Q of one row: scaled so that the largest value is in [128, 256), two E4M3 terms
     auto load_q = [&](const PromptWork& w) {
-      const int row = w.row0 + 128 * wg + tr;
+      const int row = w.row0 + kCtaRows * rank + 128 * wg + tr;
       uint4 x[kD / 8];
       if (row < w.rows) {
         const int i = row / p.G;
@@ -563,7 +656,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(qfull(wg));
+      if (lane == 0) mbar_arrive_leader(qfull(wg));
     };
 
     bool ok = true;
@@ -573,11 +666,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     if (have) load_q(w);
     for (int k = 0; ok && have; ++k) {
       // tokens that this row sees, and those that every / any row of the tile sees
-      const int row = w.row0 + 128 * wg + tr;
+      const int row = w.row0 + kCtaRows * rank + 128 * wg + tr;
       const bool live = row < w.rows;
       const int pos = w.pos0 + row / p.G;
       const int see_lo = p.a.window > 0 ? max(0, pos - p.a.window + 1) : 0, see_hi = live ? pos + 1 : 0;
-      const int r_first = w.row0 + 128 * wg, r_last = min(w.rows, r_first + 128) - 1;
+      const int r_first = w.row0 + kCtaRows * rank + 128 * wg, r_last = min(w.rows, r_first + 128) - 1;
       const int all_hi = w.pos0 + r_first / p.G + 1;
       const int all_lo = p.a.window > 0 ? w.pos0 + r_last / p.G - p.a.window + 1 : 0;
       float M = -INFINITY, l = 0.0f;
@@ -680,7 +773,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           __syncwarp();
           if (lane == 0) {
             if (half == 1) mbar_arrive(iempty(si));
-            mbar_arrive(pfull(wg, half));
+            mbar_arrive_leader(pfull(wg, half));
           }
         }
       }
@@ -700,10 +793,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           tmem_ld32(tO + c, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[(c + i) * kBlockRows] = __uint_as_float(v[i]);
+          for (int i = 0; i < 32; ++i) o[(c + i) * kCtaRows] = __uint_as_float(v[i]);
         }
-        o[kD * kBlockRows] = M;
-        o[(kD + 1) * kBlockRows] = l;
+        o[kD * kCtaRows] = M;
+        o[(kD + 1) * kCtaRows] = l;
       } else {
         const int i = row / p.G;
         uint16_t* o = static_cast<uint16_t*>(p.a.out) + (int64_t)(w.q0 + i) * p.a.out_token_stride +
@@ -746,8 +839,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     }
   };
-  if (warp == 1) {
-    mma_commit_warp(drain);
+  if (warp == 1 && rank == 0) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(drain)
+        : "memory");
     drain_wait(drain, 0);
   }
   if (warp == 0 && lane == 0 && *abort_flag) {
@@ -759,45 +855,48 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   tc_fence_before_sync();
   __syncthreads();
+  cluster_sync();                  // the leader's products no longer use the peer's memory
   if (warp == 1) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, 512);
+    pair_tmem_dealloc(tmem, 512);
   }
 }
 
 // Adds the pieces of the blocks that the last round cut.  blockIdx.x: block of that round, blockIdx.y:
-// 16 values; thread = row.
+// 16 values, blockIdx.z: CTA of the pair; thread = row.
 template <int kD>
-__global__ void __launch_bounds__(kBlockRows) k_prompt_join(const PromptParams p, int ctas) {
+__global__ void __launch_bounds__(kCtaRows) k_prompt_join(const PromptParams p, int pairs) {
   using C = PromptCfg<kD>;
   grid_dep_wait();
-  const int items = *p.count * p.a.Hkv, rounds = items / ctas, rest = items - rounds * ctas;
+  const int items = *p.count * p.a.Hkv, rounds = items / pairs, rest = items - rounds * pairs;
   const int x = blockIdx.x;
   if (x >= rest) return;
-  const int item = rounds * ctas + x, f = ctas / rest;
+  const int item = rounds * pairs + x, f = pairs / rest;
   const int2 e = p.list[item / p.a.Hkv];
   PromptWork w;
   prompt_block(p, e.x, e.y, w);
   const int np = max(1, min(f, (w.t1 - w.t0) / kMinPieceTiles));
   if (np == 1) return;
-  const int h = item % p.a.Hkv, row = w.row0 + threadIdx.x;
+  const int h = item % p.a.Hkv, row = w.row0 + kCtaRows * blockIdx.z + threadIdx.x;
   if (row >= w.rows) return;
-  const float* parts = p.parts + (size_t)(x * f) * C::PartFloats + threadIdx.x;
+  // part of piece i: CTA 2 (x f + i) + rank
+  const float* parts = p.parts + (size_t)(2 * x * f + blockIdx.z) * C::PartFloats + threadIdx.x;
+  constexpr size_t kNext = 2 * (size_t)C::PartFloats;
   float M = -INFINITY;
-  for (int i = 0; i < np; ++i) M = fmaxf(M, parts[(size_t)i * C::PartFloats + kD * kBlockRows]);
+  for (int i = 0; i < np; ++i) M = fmaxf(M, parts[i * kNext + kD * kCtaRows]);
   float l = 0.0f, acc[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
   const int c0 = blockIdx.y * 16;
   for (int i = 0; i < np; ++i) {
-    const float* o = parts + (size_t)i * C::PartFloats;
-    const float m = o[kD * kBlockRows];
+    const float* o = parts + i * kNext;
+    const float m = o[kD * kCtaRows];
     // a piece whose tokens this row does not see has an empty sum
     if (m == -INFINITY) continue;
     const float wgt = m == M ? 1.0f : exp2_approx(m - M);
-    l = __fmaf_rn(o[(kD + 1) * kBlockRows], wgt, l);
+    l = __fmaf_rn(o[(kD + 1) * kCtaRows], wgt, l);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) acc[j] = __fmaf_rn(o[(c0 + j) * kBlockRows], wgt, acc[j]);
+    for (int j = 0; j < 16; ++j) acc[j] = __fmaf_rn(o[(c0 + j) * kCtaRows], wgt, acc[j]);
   }
   const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
   const int i = row / p.G;
@@ -821,7 +920,7 @@ bool prompt_fits(int T, int G, int B) {
 
 size_t prompt_workspace_bytes(int D) {
   return 256 + kMaxBlocks * sizeof(int2) + kMaxBlocks * sizeof(int) +
-         (size_t)kPromptCtas * kBlockRows * (D + 2) * 4;
+         (size_t)kPromptCtas * kCtaRows * (D + 2) * 4;
 }
 
 template <int kD>
@@ -829,8 +928,9 @@ static cudaError_t launch_prompt(const moe_kv_attention_args& a, int min_n, int*
                                  cudaStream_t s) {
   using C = PromptCfg<kD>;
   CUtensorMap tmK, tmV;
-  if (!cache_map(&tmK, a.k_codes, kD, a.page_size, a.Hkv, a.num_pages) ||
-      !cache_map(&tmV, a.v_codes, kD, a.page_size, a.Hkv, a.num_pages))
+  // K: boxes of at most 64 tokens; V: boxes of half a head's values, unswizzled
+  if (!cache_map(&tmK, a.k_codes, kD, a.page_size, a.Hkv, a.num_pages, std::min(a.page_size, kTile / 2), kD) ||
+      !cache_map(&tmV, a.v_codes, kD, a.page_size, a.Hkv, a.num_pages, a.page_size, kD / 2))
     return cudaErrorInvalidValue;
   cudaError_t err = cudaFuncSetAttribute(k_attn_prompt<kD>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem);
@@ -846,12 +946,25 @@ static cudaError_t launch_prompt(const moe_kv_attention_args& a, int min_n, int*
   p.bins = reinterpret_cast<int*>(ws + 256 + kMaxBlocks * sizeof(int2));
   p.parts = reinterpret_cast<float*>(ws + 256 + kMaxBlocks * (sizeof(int2) + sizeof(int)));
   p.status = status;
-  const int ctas = std::min(kPromptCtas, sm_count());
+  const int pairs = std::min(kPromptCtas, sm_count()) / 2;
   err = launch_pdl(k_prompt_plan, dim3(1), dim3(1024), 0, s, p);
   if (err != cudaSuccess) return err;
-  err = launch_pdl(k_attn_prompt<kD>, dim3(ctas), dim3(kPromptThreads), C::Smem, s, tmK, tmV, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kPromptThreads);
+  cfg.dynamicSmemBytes = C::Smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  err = cudaLaunchKernelEx(&cfg, k_attn_prompt<kD>, tmK, tmV, p);
   if (err != cudaSuccess) return err;
-  return launch_pdl(k_prompt_join<kD>, dim3(ctas, kD / 16), dim3(kBlockRows), 0, s, p, ctas);
+  return launch_pdl(k_prompt_join<kD>, dim3(pairs, kD / 16, 2), dim3(kCtaRows), 0, s, p, pairs);
 }
 
 cudaError_t launch_attn_prompt(const moe_kv_attention_args& a, int min_n, int* status, void* space,
