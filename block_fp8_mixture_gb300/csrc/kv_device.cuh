@@ -87,6 +87,19 @@ __device__ __forceinline__ void mma_commit_warp(uint32_t bar) {
       : "memory");
 }
 
+// Whether any of the kThreads threads at the barrier says so.
+template <int kThreads>
+__device__ __forceinline__ bool vote_any(int barrier, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "r"(barrier), "n"(kThreads)
+      : "memory");
+  return r != 0;
+}
+
 // A wait of the whole warp; the same answer in every lane.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                int* status) {

@@ -123,17 +123,6 @@ struct FewWalk {
   }
 };
 
-__device__ __forceinline__ bool vote_any(int barrier, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)pred), "r"(barrier)
-      : "memory");
-  return r != 0;
-}
-
 // 16 values per lane -> the reduction over the warp of value r = lane >> 1 (both lanes of a pair).
 template <bool kMax>
 __device__ __forceinline__ float warp_reduce16(float (&v)[16], int lane) {
@@ -719,8 +708,8 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         bool grow = false;
 #pragma unroll
         for (int r = 0; r < 16; ++r) grow |= sc[r] > m[r] + kGrow;
-        if (vote_any(1 + wg, grow || bad)) {
-          if (vote_any(1 + wg, bad)) break;
+        if (vote_any<128>(1 + wg, grow || bad)) {
+          if (vote_any<128>(1 + wg, bad)) break;
           // the maximum of some row moved: bring what is outstanding in, then rescale
           if (pending) add_output(it - 1);
           pending = false;

@@ -1,10 +1,11 @@
 // Attention over the 8-bit paged cache for many query rows per request: prompts and chunks.
 //
 // Two matrix products of 128 x 128 x D per 128-token tile and 128 rows, so the tensor cores are the
-// bound, and the exponentials come close behind.  A block is 256 rows of one request and key/value
-// head (row = token x heads that share the head + head: any group size fills the tiles), as two tiles
-// of 128 rows that share every K and V tile, so that one tile's softmax runs while the tensor cores
-// work on the other.
+// bound; the exponentials, then shared memory's bandwidth, come close behind.  A block is 512 rows of one
+// request and key/value head (row = token x heads that share the head + head: any group size fills the
+// tiles).  Two CTAs on neighbouring SMs work on it together (cta_group::2): each has two tiles of 128 rows,
+// and a product takes one tile of each, so that every K and V tile is fetched, widened and read once for
+// 512 rows.  While one pair of tiles is in the softmax the tensor cores work on the other.
 //   S = Q K^T   kind::f8f6f4: the K codes as they are; a row of Q, scaled by a power of two, as two
 //               E4M3 terms one after the other along the reduction (2 x D at twice the 16-bit rate)
 //   O += P V    kind::f16: P in FP16 from tensor memory (it takes the place of S), V codes widened to
@@ -15,13 +16,19 @@
 // multiply-add per 16 values.  M moves only when a row passes it by 2^8, so the rescaling of O is rare;
 // p' carries a factor of 2^4, which leaves FP16 its full precision down to 2^-18 of the maximum.
 //
-//   warp 0        producer: lane i fetches page i of a tile and its scales
-//   warp 1        MMA issuer
+//   warp 0        producer: lane i fetches page i of a tile (half the tokens of K, half the values of V)
+//                 and its scales
+//   warp 1        leader: MMA issuer; peer: tells the leader that its K has landed
 //   warps 4..7    V codes -> FP16
 //   warps 8..15   softmax: thread = row, one warpgroup per tile of rows
-// Work: the blocks, longest first (k_prompt_plan), go to the CTAs in rounds, forward and back; the
+// Work: the blocks, longest first (k_prompt_plan), go to the pairs in rounds, forward and back; the
 // blocks of the last, incomplete round are cut along the cache so that every SM has a piece, and
 // k_prompt_join adds the pieces in order.
+//
+// 4096 tokens after 28000, 32 / 8 heads of 128: 1.375 ms, 1.47 PFLOP/s, 78% of the measured 16-bit rate
+// (one CTA per block of 256 rows: 1.59 ms; V read past shared memory: 1.72 ms; two threads a row: 1.52 ms;
+// an issuing warp per tile of rows: 1.85 ms).  A step of 512 rows x 128 tokens takes about 3300 cycles, of
+// which the products need 2050: what is left is the chain score -> softmax -> product of each tile.
 #include <algorithm>
 
 #include "kv_device.cuh"
@@ -38,7 +45,7 @@ constexpr float kPromptGrow = 8.0f;           // log2 by which a row may pass it
 constexpr float kPromptBias = 4.0f;           // log2 of p' at the maximum
 constexpr int kMinPieceTiles = 4;             // a piece of a cut block has at least this many tiles
 // registers of the four warpgroups, launched with 128 each
-constexpr int kRegsIssue = 56, kRegsWiden = 56, kRegsSoftmax = 200;
+constexpr int kRegsIssue = 72, kRegsWiden = 40, kRegsSoftmax = 200;
 static_assert(kRegsIssue + kRegsWiden + 2 * kRegsSoftmax <= 512, "register split must fit the launch");
 
 template <int kD>
@@ -253,25 +260,6 @@ __device__ __forceinline__ void mbar_arrive_leader(uint32_t bar) {
       "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
       "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
       : "memory");
-}
-
-// mbar_wait_warp for barriers that the peer arrives on: the phase's writes are acquired cluster-wide.
-__device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                               int* status) {
-  auto done = [&] {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return r != 0;
-  };
-  bool ok = done();
-  if (!ok) ok = mbar_wait(bar, parity, abort_flag, status) && done();
-  return __all_sync(~0u, ok);
 }
 
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
@@ -496,7 +484,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       };
       auto k_ready = [&](int tile) {
         const int s = tile % C::KStages, ph = (tile / C::KStages) & 1;
-        return mbar_wait_warp(kfull(s), ph, abort_flag, status) && mbar_wait_pair(kpeer(s), ph, abort_flag, status);
+        return mbar_wait_warp(kfull(s), ph, abort_flag, status) && mbar_wait_warp(kpeer(s), ph, abort_flag, status);
       };
       // P arrives in two halves of the tile's tokens: the product of the first runs while the softmax
       // warps form the second
@@ -504,7 +492,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const uint64_t vd = rows_desc<kD>(sW + tile % C::WStages * C::WBytes);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!mbar_wait_pair(pfull(w, half), tile & 1, abort_flag, status)) return false;
+          if (!mbar_wait_warp(pfull(w, half), tile & 1, abort_flag, status)) return false;
           tc_fence_after_sync();
 #pragma unroll
           for (int k = 4 * half; k < 4 * half + 4; ++k)
@@ -514,45 +502,35 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (w == 1) pair_commit(wempty(tile % C::WStages));
         return true;
       };
+      auto w_ready = [&](int tile) {
+        return mbar_wait_warp(wfull(tile % C::WStages), (tile / C::WStages) & 1, abort_flag, status);
+      };
+      // Everything but P is waited for behind products under way, which hide what a wait costs even when
+      // it has nothing to wait for.
       PromptWork w;
       bool have = prompt_work(p, blocks, 0, w);
-      if (have) {
-        ok = mbar_wait_pair(qfull(0), 0, abort_flag, status) && k_ready(0);
-        if (ok) {
-          tc_fence_after_sync();
-          scores(0, 0);
-        }
-        ok = ok && mbar_wait_pair(qfull(1), 0, abort_flag, status);
-        if (ok) {
-          tc_fence_after_sync();
-          scores(1, 0);
-        }
-      }
+      ok = have && k_ready(0);
       while (ok && have) {
         const int nt = w.t1 - w.t0;
-        for (int t = 0; ok && t < nt; ++t, ++it) {
-          if (!mbar_wait_pair(wfull(it % C::WStages), (it / C::WStages) & 1, abort_flag, status)) {
-            ok = false;
-            break;
-          }
-          const bool more = t + 1 < nt;
-          if (!output(0, it, t == 0)) ok = false;
-          if (ok && more) {
-            ok = k_ready(it + 1);
-            if (ok) scores(0, it + 1);
-          }
-          if (ok && !output(1, it, t == 0)) ok = false;
-          if (ok && more) scores(1, it + 1);
-        }
-        ++seg;
-        have = ok && prompt_work(p, blocks, seg, w);
-        for (int r = 0; have && ok && r < 2; ++r) {
-          ok = mbar_wait_pair(qfull(r), seg & 1, abort_flag, status) && (r == 1 || k_ready(it));
+        for (int r = 0; ok && r < 2; ++r) {
+          ok = mbar_wait_warp(qfull(r), seg & 1, abort_flag, status);
           if (ok) {
             tc_fence_after_sync();
             scores(r, it);
           }
         }
+        ok = ok && w_ready(it);
+        for (int t = 0; ok && t < nt; ++t, ++it) {
+          const bool more = t + 1 < nt;
+          ok = output(0, it, t == 0) && (!more || k_ready(it + 1));
+          if (!ok) break;
+          if (more) scores(0, it + 1);
+          ok = output(1, it, t == 0) && (!more || w_ready(it + 1));
+          if (ok && more) scores(1, it + 1);
+        }
+        ++seg;
+        have = ok && prompt_work(p, blocks, seg, w);
+        if (have) ok = k_ready(it);
       }
     }
   } else if (warp < 8) {
@@ -661,7 +639,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
     bool ok = true;
     int it = 0;
-    PromptWork w, nw;
+    PromptWork w;
     bool have = prompt_work(p, blocks, 0, w);
     if (have) load_q(w);
     for (int k = 0; ok && have; ++k) {
@@ -673,9 +651,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int r_first = w.row0 + kCtaRows * rank + 128 * wg, r_last = min(w.rows, r_first + 128) - 1;
       const int all_hi = w.pos0 + r_first / p.G + 1;
       const int all_lo = p.a.window > 0 ? w.pos0 + r_last / p.G - p.a.window + 1 : 0;
+      // where the row goes: the workspace for a piece, else the output
+      const bool piece = w.part >= 0;
+      float* const part = p.parts + (size_t)max(w.part, 0) * C::PartFloats + 128 * wg + tr;
+      uint16_t* const out = static_cast<uint16_t*>(p.a.out) + (int64_t)(w.q0 + row / p.G) * p.a.out_token_stride +
+                            (int64_t)(w.h * p.G + row % p.G) * p.a.out_head_stride;
+      const int t0 = w.t0, t1 = w.t1;
       float M = -INFINITY, l = 0.0f;
-      bool more = false;
-      for (int t = w.t0; t < w.t1; ++t, ++it) {
+      for (int t = t0; t < t1; ++t, ++it) {
         const int si = it % C::Slots;
         ok = mbar_wait(ifull(si), (it / C::Slots) & 1, abort_flag, status) &&
              mbar_wait(sfull(wg), it & 1, abort_flag, status);
@@ -727,7 +710,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (__any_sync(~0u, top > M + kPromptGrow)) {
           const float mn = fmaxf(M, top);
           const float alpha = M == mn ? 1.0f : exp2_approx(M - mn);
-          if (t > w.t0) {
+          if (t > t0) {
             // O so far is relative to the old maximum
             ok = mbar_wait(ofull(wg), (it - 1) & 1, abort_flag, status);
             ok = __all_sync(~0u, ok);
@@ -779,28 +762,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
       if (!ok) break;
       // the next piece's Q goes in while the last P V runs
-      more = prompt_work(p, blocks, k + 1, nw);
-      if (more) load_q(nw);
+      have = prompt_work(p, blocks, k + 1, w);
+      if (have) load_q(w);
       ok = mbar_wait(ofull(wg), (it - 1) & 1, abort_flag, status);
       ok = __all_sync(~0u, ok);
       if (!ok) break;
       tc_fence_after_sync();
-      if (w.part >= 0) {
-        float* o = p.parts + (size_t)w.part * C::PartFloats + 128 * wg + tr;
+      if (piece) {
 #pragma unroll 1
         for (int c = 0; c < kD; c += 32) {
           uint32_t v[32];
           tmem_ld32(tO + c, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[(c + i) * kCtaRows] = __uint_as_float(v[i]);
+          for (int i = 0; i < 32; ++i) part[(c + i) * kCtaRows] = __uint_as_float(v[i]);
         }
-        o[kD * kCtaRows] = M;
-        o[(kD + 1) * kCtaRows] = l;
+        part[kD * kCtaRows] = M;
+        part[(kD + 1) * kCtaRows] = l;
       } else {
-        const int i = row / p.G;
-        uint16_t* o = static_cast<uint16_t*>(p.a.out) + (int64_t)(w.q0 + i) * p.a.out_token_stride +
-                      (int64_t)(w.h * p.G + row - i * p.G) * p.a.out_head_stride;
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
 #pragma unroll 1
         for (int c = 0; c < kD; c += 32) {
@@ -817,14 +796,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 // a row that saw nothing may have met anything in O
                 r[h] = inv != 0.0f ? pack_bf16x2(a * inv, b * inv) : 0u;
               }
-              *reinterpret_cast<uint4*>(o + c + 8 * j) = make_uint4(r[0], r[1], r[2], r[3]);
+              *reinterpret_cast<uint4*>(out + c + 8 * j) = make_uint4(r[0], r[1], r[2], r[3]);
             }
           }
         }
       }
       tc_fence_before_sync();
-      w = nw;
-      have = more;
     }
   }
 
