@@ -338,7 +338,7 @@ class MoELayer:
 
 from .kv import (  # noqa: E402  (the paged cache uses the names above)
     PAGE_SIZES, ROPE_HALF, ROPE_INTERLEAVED, ROPE_SCALE_LINEAR, ROPE_SCALE_NONE, ROPE_SCALE_RAMP,
-    KVAttentionArgs, KVCache, KVTables, KVTablesArgs, RopeAppendArgs, alloc_kv_attention_workspace,
+    KVAttentionArgs, KVCache, KVTables, KVTablesArgs, PagedAttention, RopeAppendArgs, alloc_kv_attention_workspace,
     alloc_kv_cache, alloc_kv_tables, kv_attention, kv_attention_workspace_bytes, kv_tables, max_runs,
     rope_append, rope_table)
 from .kv import SIGNATURES as _KV_SIGNATURES  # noqa: E402

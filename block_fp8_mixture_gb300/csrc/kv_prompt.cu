@@ -45,7 +45,7 @@ constexpr float kPromptGrow = 8.0f;           // log2 by which a row may pass it
 constexpr float kPromptBias = 4.0f;           // log2 of p' at the maximum
 constexpr int kMinPieceTiles = 4;             // a piece of a cut block has at least this many tiles
 // registers of the four warpgroups, launched with 128 each
-constexpr int kRegsIssue = 72, kRegsWiden = 40, kRegsSoftmax = 200;
+constexpr int kRegsIssue = 80, kRegsWiden = 32, kRegsSoftmax = 200;
 static_assert(kRegsIssue + kRegsWiden + 2 * kRegsSoftmax <= 512, "register split must fit the launch");
 
 template <int kD>
@@ -673,25 +673,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
         tmem_ld_wait();
         auto x = [&](int i) { return __uint_as_float(s[i]); };
-        // x f + lv is the score plus log2 of the V scale, in log2 units
-        float f[8], lv[8];
-#pragma unroll
-        for (int g = 0; g < 8; g += 4) {
-          const float4 a = *reinterpret_cast<const float4*>(slot.kf + g);
-          const float4 b = *reinterpret_cast<const float4*>(slot.lv + g);
-          f[g] = a.x * qs, f[g + 1] = a.y * qs, f[g + 2] = a.z * qs, f[g + 3] = a.w * qs;
-          lv[g] = b.x, lv[g + 1] = b.y, lv[g + 2] = b.z, lv[g + 3] = b.w;
-        }
+        // x f + lv is the score plus log2 of the V scale, in log2 units, with f and lv per 16 tokens; a
+        // masked tile's scores are finished here, and f is 1 and lv 0 from then on.  (f and lv are read
+        // again for the probabilities: sixteen registers less in between.)
         if (edge) {
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
+            const float f = slot.kf[g] * qs, lv = slot.lv[g];
 #pragma unroll
             for (int i = 16 * g; i < 16 * g + 16; ++i) {
               const int j = token0 + i;
-              s[i] = __float_as_uint(j >= see_lo && j < see_hi ? __fmaf_rn(x(i), f[g], lv[g]) : -INFINITY);
+              s[i] = __float_as_uint(j >= see_lo && j < see_hi ? __fmaf_rn(x(i), f, lv) : -INFINITY);
             }
-            f[g] = 1.0f;
-            lv[g] = 0.0f;
           }
         }
         float top = -INFINITY;
@@ -704,8 +697,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             m = max3(m, x(i), x(i + 1));
             m2 = max3(m2, x(i + 2), x(i + 3));
           }
-          m = max3(m, x(16 * g + 14), x(16 * g + 15));
-          top = fmaxf(top, __fmaf_rn(fmaxf(m, m2), f[g], lv[g]));
+          m = fmaxf(max3(m, x(16 * g + 14), x(16 * g + 15)), m2);
+          top = fmaxf(top, edge ? m : __fmaf_rn(m, slot.kf[g] * qs, slot.lv[g]));
         }
         if (__any_sync(~0u, top > M + kPromptGrow)) {
           const float mn = fmaxf(M, top);
@@ -730,12 +723,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           l *= alpha;
           M = mn;
         }
+        const volatile PromptSlot* vslot = &slot;
         const float base = kPromptBias - (M == -INFINITY ? 0.0f : M);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
 #pragma unroll
           for (int g = 4 * half; g < 4 * half + 4; ++g) {
-            const f32x2 f2 = pack2(f[g], f[g]), add = pack2(lv[g] + base, lv[g] + base);
+            const float fg = edge ? 1.0f : vslot->kf[g] * qs, ag = edge ? base : vslot->lv[g] + base;
+            const f32x2 f2 = pack2(fg, fg), add = pack2(ag, ag);
             f32x2 sum = 0ull;
 #pragma unroll
             for (int i = 16 * g; i < 16 * g + 16; i += 2) {
@@ -748,7 +743,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
             float s0, s1;
             unpack2(sum, s0, s1);
-            l = __fmaf_rn(s0 + s1, slot.iv[g], l);
+            l = __fmaf_rn(s0 + s1, vslot->iv[g], l);
           }
           tmem_st32(tS + 32 * half, s + 32 * half);
           tmem_st_wait();

@@ -268,3 +268,43 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, tok_start, workspace, *
     _check(load_library().moe_kv_attention(a, workspace.data_ptr(), workspace.numel(), _stream(stream)),
            "moe_kv_attention")
     return out
+
+
+class PagedAttention:
+    """Rotary embedding, 8-bit paged cache and attention of a model's layers, for up to `max_requests`
+    requests at a time.  The layers share the tables, which advance() moves one step on; each layer has
+    its own cache.  Steps are built in the second of two sets of tables, so advance() may be called (on
+    another stream, ordered after the step before it) while kernels of that step still read the first.
+
+    rope: rope_table's result or None; max_tokens: capacity of a step's added tokens (q, k and v always
+    have that many rows; rows past a step's tokens are ignored); max_q: most tokens a request adds at once.
+    """
+
+    def __init__(self, *, num_layers: int, num_pages: int, page_size: int, num_heads: int, num_kv_heads: int,
+                 head_dim: int, max_requests: int, max_pages: int, max_tokens: int, max_q: int, rope=None,
+                 layout: int = ROPE_HALF, scale_fmt: int = SCALE_FP32, sm_scale: float | None = None,
+                 window: int = 0, device="cuda"):
+        self.caches = [alloc_kv_cache(num_pages, num_kv_heads, page_size, head_dim, device)
+                       for _ in range(num_layers)]
+        self.tables, self._next = (alloc_kv_tables(max_requests, max_pages, num_pages, page_size, max_tokens,
+                                                   device) for _ in range(2))
+        self.workspace = alloc_kv_attention_workspace(num_heads, num_kv_heads, head_dim, max_q, device)
+        self.page_size, self.max_q, self.rope, self.layout = page_size, max_q, rope, layout
+        self.scale_fmt, self.sm_scale, self.window = scale_fmt, sm_scale, window
+
+    def advance(self, new_len, stream=None) -> KVTables:
+        """Take every request to new_len cached tokens (int32 device tensor; 0: finished).  tables.info says
+        on the device how many tokens were added and how many requests the pool refused."""
+        t = self.tables
+        kv_tables(t.kv_len, new_len, t.block_table, t.free_list, t.free_count, page_size=self.page_size,
+                  out=self._next, stream=stream)
+        self.tables, self._next = self._next, t
+        return self.tables
+
+    def __call__(self, layer: int, q, k, v, out=None, stream=None):
+        """Write the step's k and v [max_tokens, Hkv, D] to the layer's cache and return the attention of
+        q [max_tokens, Hq, D] over it."""
+        t, cache = self.tables, self.caches[layer]
+        q = rope_append(q, k, v, self.rope, t, cache, layout=self.layout, scale_fmt=self.scale_fmt, stream=stream)
+        return kv_attention(q, cache, t.block_table, t.kv_len, t.tok_start, self.workspace, max_q=self.max_q,
+                            sm_scale=self.sm_scale, window=self.window, out=out, stream=stream)

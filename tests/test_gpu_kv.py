@@ -428,3 +428,51 @@ def test_attention_many_requests_and_long_cache():
     check_attention(*case, max_q=1)
     case = attention_case(rng, [70001], [1], 128, 2, 1, 64, poison=False)
     check_attention(*case, max_q=1)
+
+
+# ------------------------------------------------------------------------------- the pieces together
+def test_paged_attention_over_steps():
+    """PagedAttention over steps that add, finish, refill and roll back requests, on two layers: every
+    step's attention against the CPU statement over the cache as the library left it, and the tables
+    against theirs."""
+    rng = np.random.default_rng(21)
+    B, P, W, N, T, Hq, Hkv, D = 4, 16, 8, 20, 150, 4, 2, 64
+    attn = moe.PagedAttention(num_layers=2, num_pages=N, page_size=P, num_heads=Hq, num_kv_heads=Hkv, head_dim=D,
+                              max_requests=B, max_pages=W, max_tokens=T, max_q=T, rope=moe.rope_table(W * P, D),
+                              scale_fmt=moe.SCALE_FP32_POW2)
+    held = dict(block_table=np.full((B, W), -1), free_list=np.arange(N), free_count=[N], kv_len=np.zeros(B, int))
+    for new in ([90, 0, 20, 1], [91, 30, 21, 2], [92, 31, 0, 3], [85, 32, 100, 4], [86, 0, 101, 120], [87, 5, 102, 0]):
+        t = attn.advance(dev(np.array(new, np.int32)))
+        ref = kv_ref.kv_tables(held["kv_len"], new, held["block_table"], held["free_list"], held["free_count"][0],
+                               P, T, t.run_tok.shape[0])
+        for name, x in t._asdict().items():
+            assert np.array_equal(x.cpu().numpy(), ref[name]), name
+        held = ref
+        for layer in range(2):
+            qkv, x = bf16(rng, T, (Hq + 2 * Hkv) * D)
+            q, k, v = (a.unflatten(1, (-1, D)) for a in qkv.split([Hq * D, Hkv * D, Hkv * D], 1))
+            got = attn(layer, q, k, v).float().cpu().numpy().astype(np.float64)
+            assert moe.last_device_status(attn.workspace) == moe.MOE_OK
+            c = attn.caches[layer]
+            xq = oracle.bf16_round(kv_ref.rotate(np.split(x, [Hq * D], 1)[0].reshape(T, Hq, D), attn.rope.cpu().numpy(),
+                                                 ref["position"], 0))
+            want, mag = kv_ref.attention(xq, [a.cpu().numpy() for a in c[:2]], [a.cpu().numpy() for a in c[2:]],
+                                         ref["block_table"], ref["kv_len"], ref["tok_start"], D ** -0.5)
+            # a refused request's rows stand at positions that it does not hold: the caller drops them
+            n = int(ref["tok_start"][-1])
+            keep = ref["slot"][:n] >= 0
+            err = np.abs(got[:n] - want[:n]) - (2.0 ** -8 * np.abs(want[:n]) + 2.0 ** -9 * mag[:n])
+            assert err[keep].max(initial=-1) <= 0
+
+
+def test_decoder_block_example():
+    """The example runs, and the 8-bit cache stays near unquantized attention: a code is within 2^-4 of its
+    value (half a unit in the last of 4 bits), so keys move scores by at most 2^-4 sum |q k| sm_scale (below
+    0.2 here, 0.05 rms) and values move the output by 2^-4 / sqrt(3) rms relative: 0.1 bounds both."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decoder_block.py")
+    spec = importlib.util.spec_from_file_location("decoder_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    assert mod.main(seed=3, verbose=False) < 0.1
