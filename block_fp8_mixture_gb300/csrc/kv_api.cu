@@ -131,12 +131,11 @@ moe_status moe_kv_attention(const moe_kv_attention_args* a, void* workspace, siz
   const int G = a->Hq / a->Hkv, rows = few_rows(G, a->max_q);
   const bool prompts = (long long)G * a->max_q > rows;   // some request may have more rows than that
   if (prompts && !prompt_fits(a->T, G, a->B)) return MOE_ERR_UNSUPPORTED_SHAPE;
-  cudaError_t err = launch_attn_few(c, rows, workspace, (cudaStream_t)stream);
-  if (err == cudaSuccess && prompts) {
-    const size_t few = (few_workspace_bytes(a->D, rows) + 255) & ~(size_t)255;
-    err = launch_attn_prompt(c, rows / G, static_cast<int*>(workspace),
-                             static_cast<uint8_t*>(workspace) + few, (cudaStream_t)stream);
-  }
+  const size_t few = (few_workspace_bytes(a->D, rows) + 255) & ~(size_t)255;
+  void* space = prompts ? static_cast<uint8_t*>(workspace) + few : nullptr;
+  cudaError_t err = launch_attn_few(c, rows, workspace, space, (cudaStream_t)stream);
+  if (err == cudaSuccess && prompts)
+    err = launch_attn_prompt(c, static_cast<int*>(workspace), space, (cudaStream_t)stream);
   return launched(err);
 }
 

@@ -25,7 +25,7 @@
 // all threads of the warpgroup reduce the tile's maximum and rescale, else a vote is all it costs.
 #include <algorithm>
 
-#include "kv_device.cuh"
+#include "kv_plan.cuh"
 
 namespace moe {
 
@@ -78,9 +78,11 @@ struct FewParams {
   moe_kv_attention_args a;
   int G;                       // query heads per key/value head
   int page_shift;
-  float* parts;                // [2 * gridDim.x][kNR * (kD + 2)]
-  int* arrived;                // [gridDim.x][4] per item that a CTA leaves open and 16 rows: parts done
+  float* parts;                // [2 * ctas][kNR * (kD + 2)]
+  int* arrived;                // [ctas][4] per item that a CTA leaves open and 16 rows: parts done
   int* status;
+  int ctas;                    // CTAs that share the tiles; with a plan they follow one that lays it out
+  PromptPlan plan;
 };
 
 // Lengths of request b: cached tokens, query tokens, whether this kernel handles it, and the tiles
@@ -281,6 +283,12 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* status = p.status;
 
+  const int cta = (int)blockIdx.x - (p.plan.list != nullptr ? 1 : 0);
+  if (cta < 0) {
+    grid_dep_wait();
+    prompt_plan(p.a, p.plan, p.G, p.page_shift, reinterpret_cast<int*>(smem));
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::Stages; ++s) {
       mbar_init(kfull(s), 1);
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
     total += scan[w];
   }
   // no more CTAs than units, so the CTAs that share an item are neighbours
-  const long long ctas = max(1ll, min((long long)gridDim.x, total)), c = blockIdx.x;
+  const long long ctas = max(1ll, min((long long)p.ctas, total)), c = cta;
   const long long u0 = c < ctas ? total * c / ctas : 0, u1 = c < ctas ? total * (c + 1) / ctas : 0;
   if (u0 < u1 && u0 >= pre && u0 < pre + mine) {
     long long at = pre;
@@ -484,7 +492,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
                 const long long begin = u1 - now.left - now.tile - kItemUnits;
                 const int first = cta_of(begin + kItemUnits);
                 const int n = cta_of(begin + kItemUnits + now.item.tiles - 1) - first + 1;
-                slot.part = n == 1 ? -1 : 2 * (int)blockIdx.x + (now.seg > 0 ? 1 : 0);
+                slot.part = n == 1 ? -1 : 2 * cta + (now.seg > 0 ? 1 : 0);
                 slot.first_cta = first;
                 slot.parts = n;
                 slot.first_part = 2 * first + (total * first / ctas < begin ? 1 : 0);
@@ -892,7 +900,7 @@ size_t few_workspace_bytes(int D, int nr) {
 }
 
 template <int kD, int kNR>
-static cudaError_t launch(const moe_kv_attention_args& a, void* workspace, cudaStream_t s) {
+static cudaError_t launch(const moe_kv_attention_args& a, void* workspace, void* plan, cudaStream_t s) {
   using C = FewCfg<kD, kNR>;
   CUtensorMap tmK, tmV;
   if (!cache_map(&tmK, a.k_codes, kD, a.page_size, a.Hkv, a.num_pages, a.page_size, kD) ||
@@ -910,15 +918,20 @@ static cudaError_t launch(const moe_kv_attention_args& a, void* workspace, cudaS
   p.status = reinterpret_cast<int*>(ws);
   p.arrived = reinterpret_cast<int*>(ws + 256);
   p.parts = reinterpret_cast<float*>(ws + 256 + (size_t)few_ctas(kNR) * 16);
+  p.ctas = ctas - (plan != nullptr ? 1 : 0);   // all of the grid at once on the SMs
+  p.plan = PromptPlan{};
+  if (plan != nullptr) p.plan = prompt_plan_at(plan);
+  p.plan.min_n = kNR / p.G;
+  static_assert(C::Smem - 1024 >= kPlanSmem, "shared memory");
   return launch_pdl(k_attn_few<kD, kNR>, dim3(ctas), dim3(C::Threads), C::Smem, s, tmK, tmV, p);
 }
 
-cudaError_t launch_attn_few(const moe_kv_attention_args& a, int nr, void* workspace, cudaStream_t s) {
+cudaError_t launch_attn_few(const moe_kv_attention_args& a, int nr, void* workspace, void* plan, cudaStream_t s) {
   if (a.D == 128)
-    return nr == 16 ? launch<128, 16>(a, workspace, s)
-           : nr == 32 ? launch<128, 32>(a, workspace, s) : launch<128, 64>(a, workspace, s);
-  return nr == 16 ? launch<64, 16>(a, workspace, s)
-         : nr == 32 ? launch<64, 32>(a, workspace, s) : launch<64, 64>(a, workspace, s);
+    return nr == 16 ? launch<128, 16>(a, workspace, plan, s)
+           : nr == 32 ? launch<128, 32>(a, workspace, plan, s) : launch<128, 64>(a, workspace, plan, s);
+  return nr == 16 ? launch<64, 16>(a, workspace, plan, s)
+         : nr == 32 ? launch<64, 32>(a, workspace, plan, s) : launch<64, 64>(a, workspace, plan, s);
 }
 
 }  // namespace moe

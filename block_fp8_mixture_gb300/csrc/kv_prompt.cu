@@ -21,7 +21,7 @@
 //   warp 1        leader: MMA issuer; peer: tells the leader that its K has landed
 //   warps 4..7    V codes -> FP16
 //   warps 8..15   softmax: thread = row, one warpgroup per tile of rows
-// Work: the blocks, longest first (k_prompt_plan), go to the pairs in rounds, forward and back; the
+// Work: the blocks, longest first (kv_plan.cuh), go to the pairs in rounds, forward and back; the
 // blocks of the last, incomplete round are cut along the cache so that every SM has a piece, and
 // k_prompt_join adds the pieces in order.
 //
@@ -31,16 +31,12 @@
 // which the products need 2050: what is left is the chain score -> softmax -> product of each tile.
 #include <algorithm>
 
-#include "kv_device.cuh"
+#include "kv_plan.cuh"
 
 namespace moe {
 
-constexpr int kBlockRows = 512;              // of a pair of CTAs
-constexpr int kCtaRows = 256;
 constexpr int kPromptThreads = 512;
 constexpr int kPromptCtas = 152;              // at most (SMs)
-constexpr int kMaxBlocks = 1 << 16;           // blocks of a call, without the heads
-constexpr int kBins = 4096;                   // lengths that the order tells apart
 constexpr float kPromptGrow = 8.0f;           // log2 by which a row may pass its maximum
 constexpr float kPromptBias = 4.0f;           // log2 of p' at the maximum
 constexpr int kMinPieceTiles = 4;             // a piece of a cut block has at least this many tiles
@@ -70,34 +66,11 @@ struct PromptSlot {
 
 struct PromptParams {
   moe_kv_attention_args a;
-  int G, page_shift, min_n;
-  int2* list;                  // blocks (request, block), longest first
-  int* bins;                   // scratch of the order
-  int* count;                  // blocks
+  PromptPlan plan;
+  int G, page_shift;
   float* parts;                // [CTA][PartFloats]
   int* status;
 };
-
-// One block's rows and the tokens that they see; tiles [t0, t1) of it for this pair of CTAs.
-struct PromptWork {
-  int b, h, row0, rows, q0, pos0, lo, hi, t0, t1;
-  int part;                    // workspace part, -1: the whole block is here
-};
-
-__device__ __forceinline__ void prompt_block(const PromptParams& p, int b, int blk, PromptWork& w) {
-  w.b = b;
-  w.q0 = p.a.tok_start[b];
-  const int n = min(p.a.tok_start[b + 1] - w.q0, p.a.max_q);
-  const int L = min(max(p.a.kv_len[b], 0), p.a.max_pages << p.page_shift);
-  w.pos0 = L - (p.a.tok_start[b + 1] - w.q0);
-  w.row0 = blk * kBlockRows;
-  w.rows = n * p.G;
-  const int i0 = w.row0 / p.G, i1 = (min(w.rows, w.row0 + kBlockRows) - 1) / p.G;
-  w.hi = max(0, min(L, w.pos0 + i1 + 1));
-  w.lo = p.a.window > 0 ? max(0, w.pos0 + i0 - p.a.window + 1) : 0;
-  w.t0 = min(w.lo, max(w.hi - 1, 0)) / kTile;
-  w.t1 = max(w.t0 + 1, (w.hi + kTile - 1) / kTile);
-}
 
 // The k-th piece of work of this pair of CTAs; false when there is none.
 __device__ __forceinline__ bool prompt_work(const PromptParams& p, int blocks, int k, PromptWork& w) {
@@ -115,8 +88,8 @@ __device__ __forceinline__ bool prompt_work(const PromptParams& p, int blocks, i
   } else {
     return false;
   }
-  const int2 e = p.list[item / p.a.Hkv];
-  prompt_block(p, e.x, e.y, w);
+  const int2 e = p.plan.list[item / p.a.Hkv];
+  prompt_block(p.a, p.G, p.page_shift, e.x, e.y, w);
   w.h = item % p.a.Hkv;
   w.part = -1;
   if (pieces > 1) {
@@ -128,95 +101,6 @@ __device__ __forceinline__ bool prompt_work(const PromptParams& p, int blocks, i
     if (np > 1) w.part = blockIdx.x;
   }
   return true;
-}
-
-// Blocks of all requests with more than min_n tokens, longest first; equal lengths keep the order of
-// requests and rows, so the order never depends on timing.
-__global__ void __launch_bounds__(1024) k_prompt_plan(const PromptParams p) {
-  __shared__ int first[kMaxRequests + 1];     // blocks before request b
-  __shared__ int hist[kBins];
-  __shared__ int sums[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  grid_dep_wait();
-  grid_dep_launch_dependents();
-  auto blocks_of = [&](int b) {
-    const int q0 = p.a.tok_start[b], n = p.a.tok_start[b + 1] - q0;
-    if (n <= p.min_n || q0 < 0 || q0 + n > p.a.T) return 0;
-    return (min(n, p.a.max_q) * p.G + kBlockRows - 1) / kBlockRows;
-  };
-  auto scan = [&](int v) {                    // inclusive sum over the block
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int t = __shfl_up_sync(~0u, v, d);
-      if (lane >= d) v += t;
-    }
-    if (lane == 31) sums[warp] = v;
-    __syncthreads();
-    int base = 0;
-    for (int w = 0; w < warp; ++w) base += sums[w];
-    __syncthreads();
-    return base + v;
-  };
-  const int per = (p.a.B + 1023) / 1024;
-  int mine = 0;
-  for (int b = tid * per; b < min(p.a.B, (tid + 1) * per); ++b) mine += blocks_of(b);
-  int at = scan(mine) - mine;
-  for (int b = tid * per; b < min(p.a.B, (tid + 1) * per); ++b) {
-    first[b] = at;
-    at += blocks_of(b);
-    if (b == p.a.B - 1) first[p.a.B] = at;
-  }
-  for (int i = tid; i < kBins; i += 1024) hist[i] = 0;
-  __syncthreads();
-  const int total = min(first[p.a.B], kMaxBlocks);
-  int shift = 0;                              // tiles per bin
-  while (((p.a.max_pages << p.page_shift) / kTile + 1) >> shift >= kBins) ++shift;
-  auto owner = [&](int x) {
-    int lo = 0, hi = p.a.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first[mid] <= x) lo = mid;
-      else hi = mid;
-    }
-    return lo;
-  };
-  for (int x = tid; x < total; x += 1024) {
-    const int b = owner(x);
-    PromptWork w;
-    prompt_block(p, b, x - first[b], w);
-    const int bin = kBins - 1 - min((w.t1 - w.t0) >> shift, kBins - 1);
-    p.bins[x] = bin;
-    atomicAdd(&hist[bin], 1);
-  }
-  __syncthreads();
-  int v[kBins / 1024], sum = 0;
-#pragma unroll
-  for (int i = 0; i < kBins / 1024; ++i) {
-    v[i] = hist[tid * (kBins / 1024) + i];
-    sum += v[i];
-  }
-  int start = scan(sum) - sum;
-#pragma unroll
-  for (int i = 0; i < kBins / 1024; ++i) {
-    hist[tid * (kBins / 1024) + i] = start;
-    start += v[i];
-  }
-  __syncthreads();
-  if (warp == 0) {
-    for (int x0 = 0; x0 < total; x0 += 32) {
-      const int x = x0 + lane;
-      const int bin = x < total ? p.bins[x] : -1;
-      const uint32_t same = __match_any_sync(~0u, bin);
-      if (x < total) {
-        const int b = owner(x);
-        p.list[hist[bin] + __popc(same & ((1u << lane) - 1))] = make_int2(b, x - first[b]);
-      }
-      __syncwarp();
-      if (x < total && lane == __ffs(same) - 1) hist[bin] += __popc(same);
-      __syncwarp();
-    }
-    if (lane == 0) *p.count = total;
-  }
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
@@ -377,7 +261,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const uint32_t tmem = *tmem_slot;
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const int blocks = *p.count;
+  const int blocks = *p.plan.count;
 
   // Tensor memory: S of row tile w (P in its first half) at 128 w, O at 256 + 128 w.
   if (warp < 4) {
@@ -840,13 +724,13 @@ template <int kD>
 __global__ void __launch_bounds__(kCtaRows) k_prompt_join(const PromptParams p, int pairs) {
   using C = PromptCfg<kD>;
   grid_dep_wait();
-  const int items = *p.count * p.a.Hkv, rounds = items / pairs, rest = items - rounds * pairs;
+  const int items = *p.plan.count * p.a.Hkv, rounds = items / pairs, rest = items - rounds * pairs;
   const int x = blockIdx.x;
   if (x >= rest) return;
   const int item = rounds * pairs + x, f = pairs / rest;
-  const int2 e = p.list[item / p.a.Hkv];
+  const int2 e = p.plan.list[item / p.a.Hkv];
   PromptWork w;
-  prompt_block(p, e.x, e.y, w);
+  prompt_block(p.a, p.G, p.page_shift, e.x, e.y, w);
   const int np = max(1, min(f, (w.t1 - w.t0) / kMinPieceTiles));
   if (np == 1) return;
   const int h = item % p.a.Hkv, row = w.row0 + kCtaRows * blockIdx.z + threadIdx.x;
@@ -890,13 +774,10 @@ bool prompt_fits(int T, int G, int B) {
   return (long long)T * G / kBlockRows + B <= kMaxBlocks;
 }
 
-size_t prompt_workspace_bytes(int D) {
-  return 256 + kMaxBlocks * sizeof(int2) + kMaxBlocks * sizeof(int) +
-         (size_t)kPromptCtas * kCtaRows * (D + 2) * 4;
-}
+size_t prompt_workspace_bytes(int D) { return kPlanBytes + (size_t)kPromptCtas * kCtaRows * (D + 2) * 4; }
 
 template <int kD>
-static cudaError_t launch_prompt(const moe_kv_attention_args& a, int min_n, int* status, void* space,
+static cudaError_t launch_prompt(const moe_kv_attention_args& a, int* status, void* space,
                                  cudaStream_t s) {
   using C = PromptCfg<kD>;
   CUtensorMap tmK, tmV;
@@ -911,16 +792,10 @@ static cudaError_t launch_prompt(const moe_kv_attention_args& a, int min_n, int*
   p.a = a;
   p.G = a.Hq / a.Hkv;
   p.page_shift = __builtin_ctz((unsigned)a.page_size);
-  p.min_n = min_n;
-  uint8_t* ws = static_cast<uint8_t*>(space);
-  p.count = reinterpret_cast<int*>(ws);
-  p.list = reinterpret_cast<int2*>(ws + 256);
-  p.bins = reinterpret_cast<int*>(ws + 256 + kMaxBlocks * sizeof(int2));
-  p.parts = reinterpret_cast<float*>(ws + 256 + kMaxBlocks * (sizeof(int2) + sizeof(int)));
+  p.plan = prompt_plan_at(space);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(space) + kPlanBytes);
   p.status = status;
   const int pairs = std::min(kPromptCtas, sm_count()) / 2;
-  err = launch_pdl(k_prompt_plan, dim3(1), dim3(1024), 0, s, p);
-  if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kPromptThreads);
@@ -939,10 +814,8 @@ static cudaError_t launch_prompt(const moe_kv_attention_args& a, int min_n, int*
   return launch_pdl(k_prompt_join<kD>, dim3(pairs, kD / 16, 2), dim3(kCtaRows), 0, s, p, pairs);
 }
 
-cudaError_t launch_attn_prompt(const moe_kv_attention_args& a, int min_n, int* status, void* space,
-                               cudaStream_t s) {
-  return a.D == 128 ? launch_prompt<128>(a, min_n, status, space, s)
-                    : launch_prompt<64>(a, min_n, status, space, s);
+cudaError_t launch_attn_prompt(const moe_kv_attention_args& a, int* status, void* space, cudaStream_t s) {
+  return a.D == 128 ? launch_prompt<128>(a, status, space, s) : launch_prompt<64>(a, status, space, s);
 }
 
 }  // namespace moe
