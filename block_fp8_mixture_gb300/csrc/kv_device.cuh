@@ -87,6 +87,24 @@ __device__ __forceinline__ void mma_commit_warp(uint32_t bar) {
       : "memory");
 }
 
+// Bounded wait for the phase of `bar` with the given parity, as mbar_wait, in few instructions: the kernels
+// wait in some forty places, and code that outgrows the instruction cache is fetched at every turn.  (A
+// try_wait suspends the thread for a while by itself, so the checks between two cost nothing.)
+__device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      atomicCAS(status, 0, (int)MOE_ERR_DEVICE_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
 // Whether any of the kThreads threads at the barrier says so.
 template <int kThreads>
 __device__ __forceinline__ bool vote_any(int barrier, bool pred) {
@@ -103,7 +121,7 @@ __device__ __forceinline__ bool vote_any(int barrier, bool pred) {
 // A wait of the whole warp; the same answer in every lane.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                int* status) {
-  return __all_sync(~0u, mbar_wait(bar, parity, abort_flag, status));
+  return __all_sync(~0u, bounded_wait(bar, parity, abort_flag, status));
 }
 
 // Offset of byte x of row r in K-major rows of kRow bytes with the 128- or 64-byte swizzle.

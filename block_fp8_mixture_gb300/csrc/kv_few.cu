@@ -222,7 +222,7 @@ __device__ __forceinline__ void join_rows(const FewParams& p, int first, int res
       for (int v = 0; v < kV; ++v) acc[r][v] *= alpha;
     }
     const int k1 = min(32, n - i0);
-#pragma unroll(16 / kRows)
+#pragma unroll(8 / kRows)
     for (int k = 0; k < k1; ++k) {
       const float* o = part(i0 + k) + lane * kV;
 #pragma unroll
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           const bool mine = group == k;
           bool here = true;
           if (mine && leader) {
-            here = mbar_wait(empty(s), ((it / C::Stages) & 1) ^ 1, abort_flag, status);
+            here = bounded_wait(empty(s), ((it / C::Stages) & 1) ^ 1, abort_flag, status);
             if (here) {
               mbar_arrive_expect_tx(kfull(s), bytes);
               mbar_arrive_expect_tx(vfull(s), bytes);
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       // so no barrier is left waiting.
       bool pending = false, bad = false, begin = true;
       auto add_output = [&](int it) {                   // O of tile it
-        if (!mbar_wait(ofull, it & 1, abort_flag, status)) {
+        if (!bounded_wait(ofull, it & 1, abort_flag, status)) {
           bad = true;
           return;
         }
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       load_q(cur.item.n * p.G, cur.item.q0, cur.h);   // the first segment's, before the producer has its pages
       for (int it = 0;; ++it) {
         const int s = it % C::Stages;
-        if (!mbar_wait(ifull(s), (it / C::Stages) & 1, abort_flag, status)) bad = true;
+        if (!bounded_wait(ifull(s), (it / C::Stages) & 1, abort_flag, status)) bad = true;
         const FewSlot& slot = slots[s];
         const int rows = bad ? 0 : slot.rows, pos0 = slot.pos0, q0 = slot.q0, head = slot.head;
         if (begin) {
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         from = min(max(from - r0, 0), 16);
         to = min(max(to - r0, 0), 16);
         const uint32_t seen = to > from ? ((1u << to) - (1u << from)) : 0u;
-        if (!mbar_wait(sfull(it & 1), (it >> 1) & 1, abort_flag, status)) bad = true;
+        if (!bounded_wait(sfull(it & 1), (it >> 1) & 1, abort_flag, status)) bad = true;
         tc_fence_after_sync();
         float sc[16];
         {
@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
               make_uint4(term[k][0], term[k][1], term[k][2], term[k][3]);
         if (edge && wg == 0) {
           // V rows that no query row sees may hold anything: 0 x NaN would spread
-          if (!mbar_wait(vfull(s), (it / C::Stages) & 1, abort_flag, status)) bad = true;
+          if (!bounded_wait(vfull(s), (it / C::Stages) & 1, abort_flag, status)) bad = true;
           if (j < slot.lo || j >= slot.hi) {
             uint4* row = reinterpret_cast<uint4*>(smem + s * C::StageBytes + C::HalfBytes + tl * kD);
 #pragma unroll
@@ -785,7 +785,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           // ------------------------------------------------------- end of the segment
           if (!(flags & 4)) {                  // the next segment's, while the last P V runs
             const int ns = (it + 1) % C::Stages;
-            if (!mbar_wait(ifull(ns), ((it + 1) / C::Stages) & 1, abort_flag, status)) bad = true;
+            if (!bounded_wait(ifull(ns), ((it + 1) / C::Stages) & 1, abort_flag, status)) bad = true;
             load_q(bad ? 0 : slots[ns].rows, slots[ns].q0, slots[ns].head);
           }
           add_output(it);

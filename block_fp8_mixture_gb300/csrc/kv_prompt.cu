@@ -51,9 +51,10 @@ struct PromptCfg {
   static constexpr int KBytes = kTile / 2 * kD;          // K codes: this CTA's half of the tokens
   static constexpr int VBytes = kTile * kD / 2;          // V codes: this CTA's half of the values
   static constexpr int WBytes = 2 * VBytes;              // the same in FP16
-  static constexpr int KStages = 4, VStages = 3, WStages = 3, Slots = 6;
+  static constexpr int KStages = 4, VStages = 3, WStages = 3, Slots = 6, Works = 4;
   static constexpr int Tiles = QBytes + KStages * KBytes + VStages * VBytes + WStages * WBytes;
-  static constexpr int Smem = 1024 + Tiles + 1024 + Slots * 128;
+  static constexpr int OutWarp = 32 * 64 * 2;            // 64 BF16 values of a warp's rows on their way out
+  static constexpr int Smem = 1024 + Tiles + 8 * OutWarp + 1024 + Slots * 128 + Works * 64 + kCtaRows * 4;
   static constexpr int PartFloats = kCtaRows * (kD + 2);
   static_assert(Smem <= 232448, "shared memory");
 };
@@ -68,9 +69,14 @@ struct PromptParams {
   moe_kv_attention_args a;
   PromptPlan plan;
   int G, page_shift;
+  uint32_t magic;              // ceil(2^32 / G), 0 for G = 1: row / G is a multiply for row < 2^26
   float* parts;                // [CTA][PartFloats]
   int* status;
 };
+
+__device__ __forceinline__ int token_of(const PromptParams& p, int row) {
+  return p.magic ? (int)__umulhi((uint32_t)row, p.magic) : row;
+}
 
 // The k-th piece of work of this pair of CTAs; false when there is none.
 __device__ __forceinline__ bool prompt_work(const PromptParams& p, int blocks, int k, PromptWork& w) {
@@ -199,8 +205,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint8_t* smem = smem_raw + (sbase - raw);
   const uint32_t sQ = sbase, sK = sQ + C::QBytes, sV = sK + C::KStages * C::KBytes,
                  sW = sV + C::VStages * C::VBytes;
-  uint8_t* ctrl = smem + C::Tiles;
+  uint8_t* ctrl = smem + C::Tiles + 8 * C::OutWarp;
   PromptSlot* slots = reinterpret_cast<PromptSlot*>(ctrl + 1024);
+  int4* works = reinterpret_cast<int4*>(ctrl + 1024 + C::Slots * 128);
+  float* qscales = reinterpret_cast<float*>(ctrl + 1024 + C::Slots * 128 + C::Works * 64);   // [row]
   const uint32_t bar0 = smem_addr(ctrl);
   const int rank = (int)cluster_rank();
   auto kfull = [&](int s) { return bar0 + 8u * s; };
@@ -218,8 +226,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   auto qfull = [&](int w) { return bar0 + 8u * (76 + w); };
   auto pfull = [&](int w, int half) { return bar0 + 8u * (78 + 2 * w + half); };
   const uint32_t drain = bar0 + 8u * 82;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * 83);
-  static_assert(8 * 83 + 16 <= 1024 && C::KStages <= 8 && C::Slots <= 8, "barriers");
+  auto wkfull = [&](int i) { return bar0 + 8u * (83 + i); };     // pieces of work
+  auto wkempty = [&](int i) { return bar0 + 8u * (87 + i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * 91);
+  static_assert(8 * 91 + 16 <= 1024 && C::KStages <= 8 && C::Slots <= 8, "barriers");
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* k_done = reinterpret_cast<volatile int*>(tmem_slot + 2);
   volatile int* v_done = reinterpret_cast<volatile int*>(tmem_slot + 3);
@@ -245,6 +255,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(pfull(w, 0), 8);
       mbar_init(pfull(w, 1), 8);
     }
+    for (int i = 0; i < C::Works; ++i) {
+      mbar_init(wkfull(i), 1);
+      mbar_init(wkempty(i), 13);
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
     *k_done = 0;
@@ -263,6 +277,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   grid_dep_launch_dependents();
   const int blocks = *p.plan.count;
 
+  // The producer looks the pieces of work up, ahead of everybody, and hands them on: the k-th, for a warp
+  // of another role; false when there are no more.
+  auto take = [&](int k, PromptWork& w) {
+    const int i = k % C::Works;
+    const bool ok = mbar_wait_warp(wkfull(i), (k / C::Works) & 1, abort_flag, status);
+    const int4 a = works[4 * i], b = works[4 * i + 1], c = works[4 * i + 2];
+    w = PromptWork{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z};
+    __syncwarp();
+    if (lane == 0) mbar_arrive(wkempty(i));
+    return ok && w.t1 > 0;
+  };
+
   // Tensor memory: S of row tile w (P in its first half) at 128 w, O at 256 + 128 w.
   if (warp < 4) {
     regs_down<kRegsIssue>();
@@ -274,7 +300,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       bool ok = true;
       int it = 0;
       PromptWork w;
-      for (int k = 0; ok && prompt_work(p, blocks, k, w); ++k) {
+      for (int k = 0; ok; ++k) {
+        const bool have = prompt_work(p, blocks, k, w);
+        if (!have) w.t1 = 0;
+        const int wi = k % C::Works;
+        ok = mbar_wait_warp(wkempty(wi), ((k / C::Works) & 1) ^ 1, abort_flag, status);
+        if (!ok) break;
+        if (lane == 0) {
+          works[4 * wi] = make_int4(w.b, w.h, w.row0, w.rows);
+          works[4 * wi + 1] = make_int4(w.q0, w.pos0, w.lo, w.hi);
+          works[4 * wi + 2] = make_int4(w.t0, w.t1, w.part, 0);
+          mbar_arrive(wkfull(wi));
+        }
+        __syncwarp();
+        if (!have) break;
         auto entry = [&](int tile) {
           const int pg = tile * npg + lane;
           if (tile >= w.t1 || lane >= npg || (pg << p.page_shift) >= w.hi ||
@@ -293,8 +332,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const float ks1 = scale(p.a.k_scale, page1), vs1 = scale(p.a.v_scale, page1);
           const int sk = it % C::KStages, sv = it % C::VStages, si = it % C::Slots;
           if (lane == 0)
-            ok = mbar_wait(iempty(si), ((it / C::Slots) & 1) ^ 1, abort_flag, status) &&
-                 mbar_wait(kempty(sk), ((it / C::KStages) & 1) ^ 1, abort_flag, status);
+            ok = bounded_wait(iempty(si), ((it / C::Slots) & 1) ^ 1, abort_flag, status) &&
+                 bounded_wait(kempty(sk), ((it / C::KStages) & 1) ^ 1, abort_flag, status);
           ok = __shfl_sync(~0u, (int)ok, 0);
           if (!ok) break;
           // lane i: box i of K
@@ -319,7 +358,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(ifull(si));
-            ok = mbar_wait(vempty(sv), ((it / C::VStages) & 1) ^ 1, abort_flag, status);
+            ok = bounded_wait(vempty(sv), ((it / C::VStages) & 1) ^ 1, abort_flag, status);
           }
           ok = __shfl_sync(~0u, (int)ok, 0);
           if (!ok) break;
@@ -340,7 +379,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       bool ok = true;
       int it = 0;
       PromptWork w;
-      for (int k = 0; ok && prompt_work(p, blocks, k, w); ++k) {
+      for (int k = 0; ok && take(k, w); ++k) {
         for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
           ok = mbar_wait_warp(kfull(it % C::KStages), (it / C::KStages) & 1, abort_flag, status);
           if (ok && lane == 0) mbar_arrive_leader(kpeer(it % C::KStages));
@@ -351,8 +390,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       constexpr uint32_t kIdescS = make_idesc_e4m3(256, kTile);
       // D fp32, A and B FP16, B MN-major, 256 x kD
       constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(kD >> 3) << 17) | (16u << 24);
-      bool ok = true;
-      int it = 0, seg = 0;                   // tiles whose P V has been issued, pieces begun
       // S of row tile w for tile `tile`
       auto scores = [&](int w, int tile) {
         const uint64_t kd = rows_desc<kD>(sK + tile % C::KStages * C::KBytes);
@@ -374,13 +411,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // warps form the second
       auto output = [&](int w, int tile, bool first) {
         const uint64_t vd = rows_desc<kD>(sW + tile % C::WStages * C::WBytes);
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           if (!mbar_wait_warp(pfull(w, half), tile & 1, abort_flag, status)) return false;
           tc_fence_after_sync();
 #pragma unroll
-          for (int k = 4 * half; k < 4 * half + 4; ++k)
-            pair_mma_f16_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, vd + k * kD, kIdescO, !first || k > 0);
+          for (int k = 0; k < 4; ++k)
+            pair_mma_f16_ts(tmem + 256 + 128 * w, tmem + 128 * w + 32 * half + 8 * k, vd + (4 * half + k) * kD,
+                            kIdescO, !first || half + k > 0);
         }
         pair_commit(ofull(w));
         if (w == 1) pair_commit(wempty(tile % C::WStages));
@@ -389,32 +427,43 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       auto w_ready = [&](int tile) {
         return mbar_wait_warp(wfull(tile % C::WStages), (tile / C::WStages) & 1, abort_flag, status);
       };
-      // Everything but P is waited for behind products under way, which hide what a wait costs even when
-      // it has nothing to wait for.
+      // One stream of tiles over all pieces: the scores of the next tile are issued behind the products of
+      // this one.  Where the next tile begins another piece both products come first, for its Q is some way
+      // off: the softmax warps bring it in behind their last probabilities.  All that can be is waited for
+      // behind products under way, which hide what a wait costs even when it has nothing to wait for.
       PromptWork w;
-      bool have = prompt_work(p, blocks, 0, w);
-      ok = have && k_ready(0);
-      while (ok && have) {
-        const int nt = w.t1 - w.t0;
+      int k = 0, it = -1, t = 0;
+      bool first = true, end = true, more = take(0, w), ok = more;
+      t = w.t0 - 1;
+      while (ok) {
+        // tile `it` (none yet: -1), then the scores of tile it + 1, which is the first of piece k if `end`
+#pragma unroll 1
         for (int r = 0; ok && r < 2; ++r) {
-          ok = mbar_wait_warp(qfull(r), seg & 1, abort_flag, status);
-          if (ok) {
-            tc_fence_after_sync();
-            scores(r, it);
+          if (it >= 0) ok = output(r, it, first);
+          if (ok && !end) {
+            if (r == 0) ok = k_ready(it + 1);
+            if (ok) scores(r, it + 1);
           }
         }
-        ok = ok && w_ready(it);
-        for (int t = 0; ok && t < nt; ++t, ++it) {
-          const bool more = t + 1 < nt;
-          ok = output(0, it, t == 0) && (!more || k_ready(it + 1));
-          if (!ok) break;
-          if (more) scores(0, it + 1);
-          ok = output(1, it, t == 0) && (!more || w_ready(it + 1));
-          if (ok && more) scores(1, it + 1);
+        if (!ok) break;
+        if (end) {
+          if (it >= 0) {
+            more = take(++k, w);
+            t = w.t0 - 1;
+          }
+          if (!more || !k_ready(it + 1)) break;
+#pragma unroll 1
+          for (int r = 0; ok && r < 2; ++r) {
+            ok = mbar_wait_warp(qfull(r), k & 1, abort_flag, status);
+            tc_fence_after_sync();
+            if (ok) scores(r, it + 1);
+          }
         }
-        ++seg;
-        have = ok && prompt_work(p, blocks, seg, w);
-        if (have) ok = k_ready(it);
+        ok = ok && w_ready(it + 1);
+        first = end;
+        ++it;
+        ++t;
+        end = t + 1 == w.t1;
       }
     }
   } else if (warp < 8) {
@@ -426,11 +475,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     bool ok = true;
     int it = 0;
     PromptWork w;
-    for (int k = 0; ok && prompt_work(p, blocks, k, w); ++k) {
+    for (int k = 0; ok && take(k, w); ++k) {
       for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
         const int sv = it % C::VStages, sw = it % C::WStages;
-        ok = mbar_wait(vfull(sv), (it / C::VStages) & 1, abort_flag, status) &&
-             mbar_wait(wempty(sw), ((it / C::WStages) & 1) ^ 1, abort_flag, status);
+        ok = bounded_wait(vfull(sv), (it / C::VStages) & 1, abort_flag, status) &&
+             bounded_wait(wempty(sw), ((it / C::WStages) & 1) ^ 1, abort_flag, status);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
         const uint8_t* in = smem + (sV - sbase) + sv * C::VBytes;
@@ -470,82 +519,98 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const uint32_t tS = tmem + lane_base + 128 * wg, tO = tmem + lane_base + 256 + 128 * wg;
     float qs = 0.0f;                         // value of a code of the row's Q
 
-    // Q of one row: scaled so that the largest value is in [128, 256), two E4M3 terms
+    // Q of the warp's rows: each scaled so that its largest value is in [128, 256), two E4M3 terms.  Eight
+    // lanes a row, four rows at a time: whole lines at each load, where a row a lane would touch 32.
     auto load_q = [&](const PromptWork& w) {
-      const int row = w.row0 + kCtaRows * rank + 128 * wg + tr;
-      uint4 x[kD / 8];
-      if (row < w.rows) {
-        const int i = row / p.G;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(p.a.q) + (int64_t)(w.q0 + i) * p.a.q_token_stride +
-            (int64_t)(w.h * p.G + row - i * p.G) * p.a.q_head_stride);
-#pragma unroll
-        for (int v = 0; v < kD / 8; ++v) x[v] = src[v];
-      } else {
-#pragma unroll
-        for (int v = 0; v < kD / 8; ++v) x[v] = make_uint4(0, 0, 0, 0);
-      }
-      float amax = 0.0f;
-#pragma unroll
-      for (int v = 0; v < kD / 8; ++v) {
-        const uint32_t u[4] = {x[v].x, x[v].y, x[v].z, x[v].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
-      }
-      const int e = amax > 0.0f ? max((int)(__float_as_uint(amax) >> 23) - 127, -100) : 0;
-      const float mul = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-      qs = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
+      constexpr int kV = kD / 8;             // values of a lane
+      const int c = lane & 7;
       uint8_t* o = smem + wg * 2 * C::QTerm;
+      // four loads under way at a time (all eight at once cost more in code than they save in waiting)
+      const int base = w.row0 + kCtaRows * rank + 128 * wg + 32 * q + (lane >> 3);
+      uint4 all[4][kV / 8];
+#pragma unroll 1
+      for (int n0 = 0; n0 < 8; n0 += 4) {
 #pragma unroll
-      for (int c = 0; c < kD / 16; ++c) {
-        uint32_t t1[4], t2[4];
+        for (int n = 0; n < 4; ++n) {
+          const int row = min(base + 4 * (n0 + n), w.rows - 1), i = token_of(p, row);
+          const uint4* src = reinterpret_cast<const uint4*>(
+              static_cast<const uint16_t*>(p.a.q) + (int64_t)(w.q0 + i) * p.a.q_token_stride +
+              (int64_t)(w.h * p.G + row - i * p.G) * p.a.q_head_stride + c * kV);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 y = x[2 * c + (j >> 1)];
-          const uint32_t u0 = j & 1 ? y.z : y.x, u1 = j & 1 ? y.w : y.y;
-          const float a0 = __uint_as_float(u0 << 16) * mul, a1 = __uint_as_float(u0 & 0xFFFF0000u) * mul;
-          const float a2 = __uint_as_float(u1 << 16) * mul, a3 = __uint_as_float(u1 & 0xFFFF0000u) * mul;
-          const uint32_t c0 = cvt_e4m3x2(a0, a1), c1 = cvt_e4m3x2(a2, a3);
-          float f0, f1, f2, f3;
-          e4m3x2_to_f32(c0, f0, f1);
-          e4m3x2_to_f32(c1, f2, f3);
-          t1[j] = c0 | (c1 << 16);
-          t2[j] = cvt_e4m3x2(a0 - f0, a1 - f1) | (cvt_e4m3x2(a2 - f2, a3 - f3) << 16);
+          for (int v = 0; v < kV / 8; ++v) all[n][v] = __ldg(src + v);
         }
-        *reinterpret_cast<uint4*>(o + swz<kD>(tr, 16 * c)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-        *reinterpret_cast<uint4*>(o + C::QTerm + swz<kD>(tr, 16 * c)) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int n = n0 + m, r = 32 * q + 4 * n + (lane >> 3);
+        uint4 x[kV / 8];
+#pragma unroll
+        for (int v = 0; v < kV / 8; ++v) x[v] = base + 4 * n < w.rows ? all[m][v] : make_uint4(0, 0, 0, 0);
+        float amax = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kV / 8; ++v) {
+          const uint32_t u[4] = {x[v].x, x[v].y, x[v].z, x[v].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+        }
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, d));
+        const int e = amax > 0.0f ? max((int)(__float_as_uint(amax) >> 23) - 127, -100) : 0;
+        const float mul = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+        if (c == 0) qscales[128 * wg + r] = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
+#pragma unroll
+        for (int v = 0; v < kV / 8; ++v) {
+          const uint32_t u[4] = {x[v].x, x[v].y, x[v].z, x[v].w};
+          uint32_t t1[2], t2[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float a0 = __uint_as_float(u[2 * j] << 16) * mul, a1 = __uint_as_float(u[2 * j] & 0xFFFF0000u) * mul;
+            const float a2 = __uint_as_float(u[2 * j + 1] << 16) * mul,
+                        a3 = __uint_as_float(u[2 * j + 1] & 0xFFFF0000u) * mul;
+            const uint32_t c0 = cvt_e4m3x2(a0, a1), c1 = cvt_e4m3x2(a2, a3);
+            float f0, f1, f2, f3;
+            e4m3x2_to_f32(c0, f0, f1);
+            e4m3x2_to_f32(c1, f2, f3);
+            t1[j] = c0 | (c1 << 16);
+            t2[j] = cvt_e4m3x2(a0 - f0, a1 - f1) | (cvt_e4m3x2(a2 - f2, a3 - f3) << 16);
+          }
+          const uint32_t at = swz<kD>(r, c * kV + 8 * v);
+          *reinterpret_cast<uint2*>(o + at) = make_uint2(t1[0], t1[1]);
+          *reinterpret_cast<uint2*>(o + C::QTerm + at) = make_uint2(t2[0], t2[1]);
+        }
+      }
       }
       fence_proxy_async_smem();
+      __syncwarp();
+      qs = qscales[128 * wg + tr];
       __syncwarp();
       if (lane == 0) mbar_arrive_leader(qfull(wg));
     };
 
     bool ok = true;
     int it = 0;
-    PromptWork w;
-    bool have = prompt_work(p, blocks, 0, w);
-    if (have) load_q(w);
-    for (int k = 0; ok && have; ++k) {
+    PromptWork w = {};
+    bool have = false;               // a piece is under way; the first turn only brings in the first Q
+    for (int k = -1; ok; ++k) {
       // tokens that this row sees, and those that every / any row of the tile sees
-      const int row = w.row0 + kCtaRows * rank + 128 * wg + tr;
-      const bool live = row < w.rows;
-      const int pos = w.pos0 + row / p.G;
+      const int row = w.row0 + kCtaRows * rank + 128 * wg + tr, tok = have ? token_of(p, row) : 0;
+      const bool live = have && row < w.rows;
+      const int pos = w.pos0 + tok;
       const int see_lo = p.a.window > 0 ? max(0, pos - p.a.window + 1) : 0, see_hi = live ? pos + 1 : 0;
       const int r_first = w.row0 + kCtaRows * rank + 128 * wg, r_last = min(w.rows, r_first + 128) - 1;
-      const int all_hi = w.pos0 + r_first / p.G + 1;
-      const int all_lo = p.a.window > 0 ? w.pos0 + r_last / p.G - p.a.window + 1 : 0;
+      const int all_hi = have ? w.pos0 + token_of(p, r_first) + 1 : 0;
+      const int all_lo = have && p.a.window > 0 ? w.pos0 + token_of(p, max(r_last, 0)) - p.a.window + 1 : 0;
       // where the row goes: the workspace for a piece, else the output
       const bool piece = w.part >= 0;
       float* const part = p.parts + (size_t)max(w.part, 0) * C::PartFloats + 128 * wg + tr;
-      uint16_t* const out = static_cast<uint16_t*>(p.a.out) + (int64_t)(w.q0 + row / p.G) * p.a.out_token_stride +
-                            (int64_t)(w.h * p.G + row % p.G) * p.a.out_head_stride;
-      const int t0 = w.t0, t1 = w.t1;
+      uint16_t* const out = static_cast<uint16_t*>(p.a.out) + (int64_t)(w.q0 + tok) * p.a.out_token_stride +
+                            (int64_t)(w.h * p.G + row - tok * p.G) * p.a.out_head_stride;
+      const int t0 = have ? w.t0 : 0, t1 = have ? w.t1 : 0;
       float M = -INFINITY, l = 0.0f;
       for (int t = t0; t < t1; ++t, ++it) {
         const int si = it % C::Slots;
-        ok = mbar_wait(ifull(si), (it / C::Slots) & 1, abort_flag, status) &&
-             mbar_wait(sfull(wg), it & 1, abort_flag, status);
+        ok = bounded_wait(ifull(si), (it / C::Slots) & 1, abort_flag, status) &&
+             bounded_wait(sfull(wg), it & 1, abort_flag, status);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
         tc_fence_after_sync();
@@ -557,18 +622,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
         tmem_ld_wait();
         auto x = [&](int i) { return __uint_as_float(s[i]); };
-        // x f + lv is the score plus log2 of the V scale, in log2 units, with f and lv per 16 tokens; a
-        // masked tile's scores are finished here, and f is 1 and lv 0 from then on.  (f and lv are read
-        // again for the probabilities: sixteen registers less in between.)
+        // x f + lv is the score plus log2 of the V scale, in log2 units, with f and lv per 16 tokens.  (They
+        // are read again for the probabilities: sixteen registers less in between.)  Masked scores are -inf;
+        // f is kept above zero so that they stay so.
         if (edge) {
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const float f = slot.kf[g] * qs, lv = slot.lv[g];
+          for (int c = 0; c < 128; c += 32) {
+            const int lo = min(max(see_lo - token0 - c, 0), 32), hi = min(max(see_hi - token0 - c, 0), 32);
+            // bits [lo, hi)
+            const uint32_t seen = hi > lo ? (0xFFFFFFFFu >> (32 - (hi - lo))) << lo : 0u;
 #pragma unroll
-            for (int i = 16 * g; i < 16 * g + 16; ++i) {
-              const int j = token0 + i;
-              s[i] = __float_as_uint(j >= see_lo && j < see_hi ? __fmaf_rn(x(i), f, lv) : -INFINITY);
-            }
+            for (int i = 0; i < 32; ++i)
+              if (!((seen >> i) & 1)) s[c + i] = __float_as_uint(-INFINITY);
           }
         }
         float top = -INFINITY;
@@ -582,14 +647,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             m2 = max3(m2, x(i + 2), x(i + 3));
           }
           m = fmaxf(max3(m, x(16 * g + 14), x(16 * g + 15)), m2);
-          top = fmaxf(top, edge ? m : __fmaf_rn(m, slot.kf[g] * qs, slot.lv[g]));
+          top = fmaxf(top, __fmaf_rn(m, fmaxf(slot.kf[g] * qs, 1.2e-38f), slot.lv[g]));
         }
         if (__any_sync(~0u, top > M + kPromptGrow)) {
           const float mn = fmaxf(M, top);
           const float alpha = M == mn ? 1.0f : exp2_approx(M - mn);
           if (t > t0) {
             // O so far is relative to the old maximum
-            ok = mbar_wait(ofull(wg), (it - 1) & 1, abort_flag, status);
+            ok = bounded_wait(ofull(wg), (it - 1) & 1, abort_flag, status);
             ok = __all_sync(~0u, ok);
             if (!ok) break;
             tc_fence_after_sync();
@@ -613,7 +678,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         for (int half = 0; half < 2; ++half) {
 #pragma unroll
           for (int g = 4 * half; g < 4 * half + 4; ++g) {
-            const float fg = edge ? 1.0f : vslot->kf[g] * qs, ag = edge ? base : vslot->lv[g] + base;
+            const float fg = fmaxf(vslot->kf[g] * qs, 1.2e-38f), ag = vslot->lv[g] + base;
             const f32x2 f2 = pack2(fg, fg), add = pack2(ag, ag);
             f32x2 sum = 0ull;
 #pragma unroll
@@ -641,9 +706,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
       if (!ok) break;
       // the next piece's Q goes in while the last P V runs
-      have = prompt_work(p, blocks, k + 1, w);
+      const bool had = have;
+      have = take(k + 1, w);
       if (have) load_q(w);
-      ok = mbar_wait(ofull(wg), (it - 1) & 1, abort_flag, status);
+      if (!had) {
+        if (!have) break;
+        continue;
+      }
+      ok = bounded_wait(ofull(wg), (it - 1) & 1, abort_flag, status);
       ok = __all_sync(~0u, ok);
       if (!ok) break;
       tc_fence_after_sync();
@@ -659,13 +729,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         part[kD * kCtaRows] = M;
         part[(kD + 1) * kCtaRows] = l;
       } else {
+        // 64 values at a time through shared memory, so that the stores cover whole lines of a row
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        uint8_t* stage = smem + C::Tiles + (4 * wg + q) * C::OutWarp;
 #pragma unroll 1
-        for (int c = 0; c < kD; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(tO + c, v);
-          tmem_ld_wait();
-          if (live) {
+        for (int c0 = 0; c0 < kD; c0 += 64) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(tO + c0 + c, v);
+            tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               uint32_t r[4];
@@ -675,12 +748,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 // a row that saw nothing may have met anything in O
                 r[h] = inv != 0.0f ? pack_bf16x2(a * inv, b * inv) : 0u;
               }
-              *reinterpret_cast<uint4*>(out + c + 8 * j) = make_uint4(r[0], r[1], r[2], r[3]);
+              *reinterpret_cast<uint4*>(stage + swz<128>(lane, 2 * c + 16 * j)) = make_uint4(r[0], r[1], r[2], r[3]);
             }
           }
+          __syncwarp();
+#pragma unroll
+          for (int r4 = 0; r4 < 32; r4 += 4) {
+            const int r = r4 + (lane >> 3);
+            const unsigned long long to = __shfl_sync(~0u, live ? (unsigned long long)out : 0ull, r);
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + swz<128>(r, 16 * (lane & 7)));
+            if (to != 0) *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(to) + c0 + 8 * (lane & 7)) = v;
+          }
+          __syncwarp();
         }
       }
       tc_fence_before_sync();
+      if (!have) break;
     }
   }
 
@@ -792,6 +875,7 @@ static cudaError_t launch_prompt(const moe_kv_attention_args& a, int* status, vo
   p.a = a;
   p.G = a.Hq / a.Hkv;
   p.page_shift = __builtin_ctz((unsigned)a.page_size);
+  p.magic = p.G == 1 ? 0 : (uint32_t)(((1ull << 32) + p.G - 1) / p.G);
   p.plan = prompt_plan_at(space);
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(space) + kPlanBytes);
   p.status = status;
