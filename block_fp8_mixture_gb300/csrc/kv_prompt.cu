@@ -41,7 +41,7 @@ constexpr float kPromptGrow = 8.0f;           // log2 by which a row may pass it
 constexpr float kPromptBias = 4.0f;           // log2 of p' at the maximum
 constexpr int kMinPieceTiles = 4;             // a piece of a cut block has at least this many tiles
 // registers of the four warpgroups, launched with 128 each
-constexpr int kRegsIssue = 80, kRegsWiden = 32, kRegsSoftmax = 200;
+constexpr int kRegsIssue = 88, kRegsWiden = 40, kRegsSoftmax = 192;
 static_assert(kRegsIssue + kRegsWiden + 2 * kRegsSoftmax <= 512, "register split must fit the launch");
 
 template <int kD>
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // warps form the second
       auto output = [&](int w, int tile, bool first) {
         const uint64_t vd = rows_desc<kD>(sW + tile % C::WStages * C::WBytes);
-#pragma unroll 1
+#pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (!mbar_wait_warp(pfull(w, half), tile & 1, abort_flag, status)) return false;
           tc_fence_after_sync();
