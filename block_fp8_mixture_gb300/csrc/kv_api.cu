@@ -113,6 +113,9 @@ moe_status moe_kv_attention(const moe_kv_attention_args* a, void* workspace, siz
   if (a->Hq % a->Hkv || a->Hq / a->Hkv > kMaxGroup || a->B > kMaxRequests ||
       (long long)a->max_pages * a->page_size > 0x7FFFFFFFll)
     return MOE_ERR_UNSUPPORTED_SHAPE;
+  // shares of the few-row kernel's tiles are counted in 32 bits
+  if (((long long)a->B * a->max_pages * a->page_size / 128 + 4ll * a->B) * a->Hkv > 0x7FFFFFFFll - (1 << 20))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!(a->sm_scale > 0.0f) || !isfinite(a->sm_scale)) return MOE_ERR_INVALID_ARG;
   if (!good(workspace, 256)) return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < moe_kv_attention_workspace_bytes(a->Hq, a->Hkv, a->D, a->max_q))

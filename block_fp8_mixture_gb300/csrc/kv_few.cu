@@ -14,10 +14,10 @@
 // The page's K scale multiplies the score, its V scale the probability, relative to the tile's largest.
 //
 // The work is dealt out evenly, whatever the lengths: an item (request, head) weighs kItemUnits, what
-// its start and end cost, and one unit per 128-token tile; CTA c takes the tiles that lie in
-// [c U / G, (c + 1) U / G) of the flattened list (G = CTAs, at most U).  A CTA that holds part of an item
-// leaves its sums, maximum and unscaled output in the workspace; the CTA that arrives last adds the parts,
-// in CTA order, so results do not depend on timing.
+// its start and end cost, and one unit per 128-token tile; CTA c takes the tiles that lie in the c-th of
+// equal shares of the flattened list.  A CTA that holds part of an item leaves its sums, maximum and
+// unscaled output in the workspace; the CTA that arrives last adds the parts, in CTA order, so results do
+// not depend on timing.
 //   warp 0      producer: lane i fetches page i of the tile (TMA), its scales and the tile's bounds
 //   warp 1      MMA issuer
 //   warps 2..   one warpgroup per 16 rows: thread = token for the scores, = d for the output
@@ -112,7 +112,7 @@ template <int kNR>
 struct FewWalk {
   int b, h, tile;
   FewItem item;
-  long long left;              // units from this tile to the CTA's end; <= 0: no tile here
+  int left;                    // units from this tile to the CTA's end; <= 0: no tile here
   __device__ __forceinline__ void next(const FewParams& p) {
     if (--left <= 0 || ++tile < item.tiles) return;
     if ((left -= kItemUnits) <= 0) return;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (kB + 6));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* mma_done = reinterpret_cast<volatile int*>(tmem_slot + 2);
-  long long* scan = reinterpret_cast<long long*>(ctrl + 8 * (kB + 6) + 16);   // [warps + 2], an item
+  int* scan = reinterpret_cast<int*>(ctrl + 8 * (kB + 6) + 16);   // [warps + 2], an item
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* status = p.status;
@@ -312,40 +312,40 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
 
   // ------------------------------------------------------------ the CTA's share of the units
   // an exclusive sum over threads with consecutive requests each
-  auto weight = [&](const FewItem& it) { return it.tiles ? (long long)(it.tiles + kItemUnits) * p.a.Hkv : 0ll; };
+  auto weight = [&](const FewItem& it) { return it.tiles ? (it.tiles + kItemUnits) * p.a.Hkv : 0; };
   grid_dep_wait();
   const int per = (p.a.B + C::Threads - 1) / C::Threads;
   const int rb0 = threadIdx.x * per, rb1 = min(p.a.B, rb0 + per);
-  long long mine = 0;
+  int mine = 0;
   for (int b = rb0; b < rb1; ++b) mine += weight(few_item<kNR>(p, b));
-  long long pre = mine;
+  int pre = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long t = __shfl_up_sync(~0u, pre, d);
+    const int t = __shfl_up_sync(~0u, pre, d);
     if (lane >= d) pre += t;
   }
   constexpr int kWarps = C::Threads / 32;
-  static_assert(8 * (kWarps + 2) + (int)sizeof(FewItem) <= 208, "scan area");
+  static_assert(4 * (kWarps + 2) + (int)sizeof(FewItem) <= 208, "scan area");
   if (lane == 31) scan[warp] = pre;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  long long total = 0;
+  int total = 0;
   pre -= mine;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) pre += scan[w];
     total += scan[w];
   }
-  // no more CTAs than units, so the CTAs that share an item are neighbours
-  const long long ctas = max(1ll, min((long long)p.ctas, total)), c = cta;
-  const long long u0 = c < ctas ? total * c / ctas : 0, u1 = c < ctas ? total * (c + 1) / ctas : 0;
+  // (the CTAs that share an item are neighbours: none between them is without units)
+  const int share = (total + p.ctas - 1) / p.ctas;
+  const int u0 = min(total, cta * share), u1 = min(total, u0 + share);
   if (u0 < u1 && u0 >= pre && u0 < pre + mine) {
-    long long at = pre;
+    int at = pre;
     for (int b = rb0; b < rb1; ++b) {
       const FewItem it = few_item<kNR>(p, b);
-      const long long w = weight(it);
+      const int w = weight(it);
       if (u0 < at + w) {
         scan[kWarps] = b;
         scan[kWarps + 1] = u0 - at;
@@ -362,9 +362,9 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
   cur.b = cur.h = cur.tile = 0;
   cur.item = FewItem{};
   if (u0 < u1) {
-    cur.b = (int)scan[kWarps];
+    cur.b = scan[kWarps];
     cur.item = *reinterpret_cast<const FewItem*>(scan + kWarps + 2);
-    const int u = (int)scan[kWarps + 1], per_item = cur.item.tiles + kItemUnits;
+    const int u = scan[kWarps + 1], per_item = cur.item.tiles + kItemUnits;
     cur.h = u / per_item;
     const int at = u - cur.h * per_item - kItemUnits;
     cur.tile = max(at, 0);
@@ -382,13 +382,6 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       const int group = lane / npg, pi = lane - group * npg;
       const int batch = min(kBatch, 32 / npg);
       const bool leader = pi == 0;
-      // the CTA that has unit x
-      auto cta_of = [&](long long x) {
-        long long k = x * ctas / total;
-        while (total * (k + 1) / ctas <= x) ++k;
-        while (total * k / ctas > x) --k;
-        return (int)k;
-      };
       int seg = 0;
       struct Ahead {
         FewItem item;
@@ -409,7 +402,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
             a.h = cur.h;
             a.tile = cur.tile;
             a.seg = seg;
-            a.left = (int)cur.left;
+            a.left = cur.left;
             a.live = 1;
           }
           if (cur.tile == cur.item.tiles - 1) ++seg;
@@ -489,13 +482,13 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
               slot.flags = (end || last ? 2 : 0) | (last ? 4 : 0);
               if (end || last) {
                 // the item's units: its own from `begin`, then its tiles
-                const long long begin = u1 - now.left - now.tile - kItemUnits;
-                const int first = cta_of(begin + kItemUnits);
-                const int n = cta_of(begin + kItemUnits + now.item.tiles - 1) - first + 1;
+                const int begin = u1 - now.left - now.tile - kItemUnits;
+                const int first = (begin + kItemUnits) / share;
+                const int n = (begin + kItemUnits + now.item.tiles - 1) / share - first + 1;
                 slot.part = n == 1 ? -1 : 2 * cta + (now.seg > 0 ? 1 : 0);
                 slot.first_cta = first;
                 slot.parts = n;
-                slot.first_part = 2 * first + (total * first / ctas < begin ? 1 : 0);
+                slot.first_part = 2 * first + (first * share < begin ? 1 : 0);
               }
             }
           }
@@ -656,7 +649,9 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         named_barrier_sync(1 + wg, 128);
         if (lane == 0) mbar_arrive(qfull);
       };
-      load_q(cur.item.n * p.G, cur.item.q0, cur.h);   // the first segment's, before the producer has its pages
+      // the segment whose Q comes next; the CTA's first is known before the producer has its pages
+      int q_rows = cur.item.n * p.G, q_q0 = cur.item.q0, q_head = cur.h;
+      load_q(q_rows, q_q0, q_head);
       for (int it = 0;; ++it) {
         const int s = it % C::Stages;
         if (!bounded_wait(ifull(s), (it / C::Stages) & 1, abort_flag, status)) bad = true;
