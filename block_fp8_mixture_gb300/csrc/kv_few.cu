@@ -33,6 +33,8 @@ constexpr float kPScale = 32.0f;           // P = 1 at the running maximum becom
 constexpr float kGrow = 3.0f;              // log2 by which a score may pass the maximum
 constexpr int kBatch = 8;                  // tiles whose pages are looked up together, at most
 constexpr int kItemUnits = 3;              // start and end of an item, in tiles
+constexpr int kJoinGroup = 16;             // CTAs whose parts are added first where an item has many parts
+constexpr int kJoinOnce = 40;              // parts x rows of a warp that are added in one step
 constexpr float kTermStep = 32.0f;         // each further E4M3 term is scaled up by this
 constexpr float kNoScore = -3e38f;         // running maximum before the first token: finite, so that
                                            // a masked score (-inf) minus it stays -inf
@@ -79,7 +81,7 @@ struct FewParams {
   int G;                       // query heads per key/value head
   int page_shift;
   float* parts;                // [2 * ctas][kNR * (kD + 2)]
-  int* arrived;                // [ctas][4] per item that a CTA leaves open and 16 rows: parts done
+  int* arrived;                // [ctas][2][4] per CTA that opens a group or an item and 16 rows: parts, groups done
   int* status;
   int ctas;                    // CTAs that share the tiles; with a plan they follow one that lays it out
   PromptPlan plan;
@@ -182,15 +184,27 @@ __device__ __forceinline__ uint64_t p_desc(uint32_t saddr) {
   return d;
 }
 
-// kRows rows of an item, from `row` on and below row1, out of its n parts: `first`, then 2 i after `rest`,
-// i = 1 .. n - 1.  One warp: the lanes read the parts' maxima and sums, then every lane its D / 32 values
-// of all rows, with as many loads under way as registers allow, for latency is all there is to it.
+// Parts of an item that are added together: n of them, every step-th from i0 on.  Part 0 of the item lies
+// at `first`, part i > 0 at rest + 2 i.  The sum goes to out if they are the whole item, else in i0's place.
+struct JoinSet {
+  int first, rest, i0, step, n;
+  bool whole;
+};
+
+// kRows rows of an item, from `row` on and below row1.  One warp: the lanes read the parts' maxima and
+// sums, then every lane its D / 32 values of all rows, with as many loads under way as registers allow,
+// for latency is all there is to it.
+constexpr int kJoinLoads = 8;
 template <int kD, int kNR, int kRows>
-__device__ __forceinline__ void join_rows(const FewParams& p, int first, int rest, int n, int row, int row1, int q0,
+__device__ __forceinline__ void join_rows(const FewParams& p, const JoinSet& set, int row, int row1, int q0,
                                           int head, int lane) {
   constexpr size_t kPart = kNR * (kD + 2);
   constexpr int kV = kD / 32;               // values of a row per lane
-  auto part = [&](int i) { return p.parts + (size_t)(i == 0 ? first : rest + 2 * i) * kPart; };
+  const int n = set.n;
+  auto part = [&](int k) {
+    const int i = set.i0 + k * set.step;
+    return p.parts + (size_t)(i == 0 ? set.first : set.rest + 2 * i) * kPart;
+  };
   float m[kRows], l[kRows], acc[kRows][kV];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
@@ -222,7 +236,7 @@ __device__ __forceinline__ void join_rows(const FewParams& p, int first, int res
       for (int v = 0; v < kV; ++v) acc[r][v] *= alpha;
     }
     const int k1 = min(32, n - i0);
-#pragma unroll(8 / kRows)
+#pragma unroll(kJoinLoads / kRows)
     for (int k = 0; k < k1; ++k) {
       const float* o = part(i0 + k) + lane * kV;
 #pragma unroll
@@ -242,6 +256,13 @@ __device__ __forceinline__ void join_rows(const FewParams& p, int first, int res
 #pragma unroll
     for (int d = 16; d; d >>= 1) l[r] += __shfl_xor_sync(~0u, l[r], d);
     if (row + r >= row1) break;
+    if (!set.whole) {
+      float* o = part(0);
+#pragma unroll
+      for (int v = 0; v < kV; ++v) o[(row + r) * kD + lane * kV + v] = acc[r][v];
+      if (lane == 0) *reinterpret_cast<float2*>(o + kNR * kD + 2 * (row + r)) = make_float2(m[r], l[r]);
+      continue;
+    }
     const float inv = l[r] > 0.0f || l[r] != l[r] ? 1.0f / l[r] : 0.0f;
     const int i = (row + r) / p.G;
     uint32_t* out = reinterpret_cast<uint32_t*>(
@@ -821,25 +842,42 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
               *reinterpret_cast<float2*>(o + kNR * kD + 2 * my_row) = make_float2(mm, lsum);
           }
           if (part >= 0) {
-            // the last of the item's CTAs to get here adds the parts
-            __threadfence();
-            named_barrier_sync(1 + wg, 128);
-            int* arrived = p.arrived + 4 * first_cta + wg;
-            if (wt == 0) {
-              const int before = atomicAdd(arrived, 1);
-              if (before == parts - 1) *arrived = 0;
-              __threadfence();
-              wred[0] = before == parts - 1 ? 1.0f : 0.0f;
-            }
-            named_barrier_sync(1 + wg, 128);
-            if (wred[0] != 0.0f) {
-              const int row1 = min(rows, r0 + 16), jw = wt >> 5;
-              if (kNR == 64 || row1 - r0 <= 4) {     // 64 rows: no registers for four at once
-                for (int row = r0 + jw; row < row1; row += 4)
-                  join_rows<kD, kNR, 1>(p, first_part, 2 * first_cta, parts, row, row1, q0, head, lane);
-              } else if (r0 + 4 * jw < row1) {
-                join_rows<kD, kNR, 4>(p, first_part, 2 * first_cta, parts, r0 + 4 * jw, row1, q0, head, lane);
+            // the last of a group of CTAs to get here adds the group's parts, the last of the groups theirs
+            const int row1 = min(rows, r0 + 16), jw = wt >> 5;
+            JoinSet set;
+            set.first = first_part;
+            set.rest = 2 * first_cta;
+            set.whole = parts <= kJoinGroup || (row1 - r0 + 3) / 4 * parts <= kJoinOnce;
+            set.i0 = set.whole ? 0 : (cta - first_cta) & -kJoinGroup;
+            set.step = 1;
+            set.n = set.whole ? parts : min(kJoinGroup, parts - set.i0);
+            int* arrived = p.arrived + 8 * (first_cta + set.i0) + wg;
+            while (true) {
+              if (set.n > 1) {
+                __threadfence();
+                named_barrier_sync(1 + wg, 128);
+                if (wt == 0) {
+                  const int before = atomicAdd(arrived, 1);
+                  if (before == set.n - 1) *arrived = 0;
+                  __threadfence();
+                  wred[0] = before == set.n - 1 ? 1.0f : 0.0f;
+                }
+                named_barrier_sync(1 + wg, 128);
+                if (wred[0] == 0.0f) break;
+                if (kNR == 64 || row1 - r0 <= 4) {   // 64 rows: no registers for more at once
+                  for (int row = r0 + jw; row < row1; row += 4)
+                    join_rows<kD, kNR, 1>(p, set, row, row1, q0, head, lane);
+                } else {
+                  for (int row = r0 + 2 * jw; row < row1; row += 8)
+                    join_rows<kD, kNR, 2>(p, set, row, row1, q0, head, lane);
+                }
               }
+              if (set.whole) break;
+              set.i0 = 0;
+              set.step = kJoinGroup;
+              set.n = (parts + kJoinGroup - 1) / kJoinGroup;
+              set.whole = true;
+              arrived = p.arrived + 8 * first_cta + 4 + wg;
             }
           }
           named_barrier_sync(1 + wg, 128);     // the sums have been read
@@ -891,7 +929,7 @@ static int few_ctas(int nr) { return nr == 16 ? 304 : 152; }   // at most; 152 S
 
 size_t few_workspace_bytes(int D, int nr) {
   const int ctas = few_ctas(nr);
-  return 256 + (size_t)ctas * 16 + (size_t)2 * ctas * nr * (D + 2) * 4;
+  return 256 + (size_t)ctas * 32 + (size_t)2 * ctas * nr * (D + 2) * 4;
 }
 
 template <int kD, int kNR>
@@ -912,7 +950,7 @@ static cudaError_t launch(const moe_kv_attention_args& a, void* workspace, void*
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.status = reinterpret_cast<int*>(ws);
   p.arrived = reinterpret_cast<int*>(ws + 256);
-  p.parts = reinterpret_cast<float*>(ws + 256 + (size_t)few_ctas(kNR) * 16);
+  p.parts = reinterpret_cast<float*>(ws + 256 + (size_t)few_ctas(kNR) * 32);
   p.ctas = ctas - (plan != nullptr ? 1 : 0);   // all of the grid at once on the SMs
   p.plan = PromptPlan{};
   if (plan != nullptr) p.plan = prompt_plan_at(plan);

@@ -430,6 +430,24 @@ def test_attention_many_requests_and_long_cache():
     check_attention(*case, max_q=1)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,ctx,add", [
+    (3, 1, 128, [12000], [1]),               # 3 rows, about 95 parts
+    (8, 1, 128, [9000, 21000], [1, 1]),      # 8 rows, items that start inside a group of parts
+    (16, 1, 64, [17000], [1]),               # 16 rows
+    (12, 2, 128, [9000, 30], [3, 2]),        # 18 rows: two sets of 16
+    (64, 1, 64, [13000], [1]),               # 64 rows
+    (5, 1, 64, [700, 24000, 10, 8000], [1, 0, 1, 2]),
+])
+def test_attention_long_items_are_joined_in_two_steps(Hq, Hkv, D, ctx, add):
+    """Items whose parts are more than one step of additions takes; the counters must be back at zero
+    after each call and the order of the additions fixed, so a second call repeats the first."""
+    rng = np.random.default_rng(Hq + D)
+    case = attention_case(rng, ctx, add, 32, Hq, Hkv, D, poison=False)
+    ws = moe.alloc_kv_attention_workspace(Hq, Hkv, D, max(add))
+    first = check_attention(*case, max_q=max(add), ws=ws).clone()
+    assert torch.equal(check_attention(*case, max_q=max(add), ws=ws), first)
+
+
 # ------------------------------------------------------------------------------- the pieces together
 def test_paged_attention_over_steps():
     """PagedAttention over steps that add, finish, refill and roll back requests, on two layers: every
