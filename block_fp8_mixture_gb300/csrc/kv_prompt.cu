@@ -21,14 +21,15 @@
 //   warp 1        leader: MMA issuer; peer: tells the leader that its K has landed
 //   warps 4..7    V codes -> FP16
 //   warps 8..15   softmax: thread = row, one warpgroup per tile of rows
-// Work: the blocks, longest first (kv_plan.cuh), go to the pairs in rounds, forward and back; the
-// blocks of the last, incomplete round are cut along the cache so that every SM has a piece, and
-// k_prompt_join adds the pieces in order.
+// Work: rounds over the blocks, longest first, and a last one whose tiles are poured over the pairs up to
+// a common level (kv_plan.cuh).  Blocks that this cuts along the cache k_prompt_join adds up, in order.
 //
 // 4096 tokens after 28000, 32 / 8 heads of 128: 1.375 ms, 1.47 PFLOP/s, 78% of the measured 16-bit rate
 // (one CTA per block of 256 rows: 1.59 ms; V read past shared memory: 1.72 ms; two threads a row: 1.52 ms;
 // an issuing warp per tile of rows: 1.85 ms).  A step of 512 rows x 128 tokens takes about 3300 cycles, of
 // which the products need 2050: what is left is the chain score -> softmax -> product of each tile.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 
 #include "kv_plan.cuh"
@@ -36,10 +37,8 @@
 namespace moe {
 
 constexpr int kPromptThreads = 512;
-constexpr int kPromptCtas = 152;              // at most (SMs)
 constexpr float kPromptGrow = 8.0f;           // log2 by which a row may pass its maximum
 constexpr float kPromptBias = 4.0f;           // log2 of p' at the maximum
-constexpr int kMinPieceTiles = 4;             // a piece of a cut block has at least this many tiles
 // registers of the four warpgroups, launched with 128 each
 constexpr int kRegsIssue = 88, kRegsWiden = 40, kRegsSoftmax = 192;
 static_assert(kRegsIssue + kRegsWiden + 2 * kRegsSoftmax <= 512, "register split must fit the launch");
@@ -55,7 +54,10 @@ struct PromptCfg {
   static constexpr int Tiles = QBytes + KStages * KBytes + VStages * VBytes + WStages * WBytes;
   static constexpr int OutWarp = 32 * 64 * 2;            // 64 BF16 values of a warp's rows on their way out
   static constexpr int Smem = 1024 + Tiles + 8 * OutWarp + 1024 + Slots * 128 + Works * 64 + kCtaRows * 4;
-  static constexpr int PartFloats = kCtaRows * (kD + 2);
+  // A part of a cut block: a row's values as FP16 after a power of two that takes the largest to 2^14 .. 2^15,
+  // with that scale, the row's maximum and its sum in FP32.  The join adds in FP32; what the 11 bits
+  // leave off is an eighth of the output's own rounding to BF16, and half the bytes are half the time.
+  static constexpr int PartWords = kCtaRows * (kD / 2 + 3);
   static_assert(Smem <= 232448, "shared memory");
 };
 
@@ -70,43 +72,12 @@ struct PromptParams {
   PromptPlan plan;
   int G, page_shift;
   uint32_t magic;              // ceil(2^32 / G), 0 for G = 1: row / G is a multiply for row < 2^26
-  float* parts;                // [CTA][PartFloats]
+  uint32_t* parts;             // [2 * pairs][CTA of the pair][PartWords]
   int* status;
 };
 
 __device__ __forceinline__ int token_of(const PromptParams& p, int row) {
   return p.magic ? (int)__umulhi((uint32_t)row, p.magic) : row;
-}
-
-// The k-th piece of work of this pair of CTAs; false when there is none.
-__device__ __forceinline__ bool prompt_work(const PromptParams& p, int blocks, int k, PromptWork& w) {
-  const int C = gridDim.x / 2, c = blockIdx.x / 2;
-  const int items = blocks * p.a.Hkv, rounds = items / C, rest = items - rounds * C;
-  int item, piece = 0, pieces = 1;
-  if (k < rounds) {
-    item = k * C + ((k & 1) ? C - 1 - c : c);
-  } else if (k == rounds && rest > 0) {
-    const int f = C / rest;
-    if (c >= rest * f) return false;
-    item = rounds * C + c / f;
-    piece = c % f;
-    pieces = f;
-  } else {
-    return false;
-  }
-  const int2 e = p.plan.list[item / p.a.Hkv];
-  prompt_block(p.a, p.G, p.page_shift, e.x, e.y, w);
-  w.h = item % p.a.Hkv;
-  w.part = -1;
-  if (pieces > 1) {
-    const int nt = w.t1 - w.t0, np = max(1, min(pieces, nt / kMinPieceTiles));
-    if (piece >= np) return false;
-    const int t0 = w.t0;
-    w.t0 = t0 + nt * piece / np;
-    w.t1 = t0 + nt * (piece + 1) / np;
-    if (np > 1) w.part = blockIdx.x;
-  }
-  return true;
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
@@ -275,7 +246,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const uint32_t tmem = *tmem_slot;
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const int blocks = *p.plan.count;
 
   // The producer looks the pieces of work up, ahead of everybody, and hands them on: the k-th, for a warp
   // of another role; false when there are no more.
@@ -300,8 +270,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       bool ok = true;
       int it = 0;
       PromptWork w;
+      const int pair = blockIdx.x / 2;
+      PromptWalk walk;
+      walk.start(p.plan, pair, lane);
       for (int k = 0; ok; ++k) {
-        const bool have = prompt_work(p, blocks, k, w);
+        const bool have = walk.next(p.a, p.plan, p.G, p.page_shift, pair, w);
         if (!have) w.t1 = 0;
         const int wi = k % C::Works;
         ok = mbar_wait_warp(wkempty(wi), ((k / C::Works) & 1) ^ 1, abort_flag, status);
@@ -602,7 +575,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int all_lo = have && p.a.window > 0 ? w.pos0 + token_of(p, max(r_last, 0)) - p.a.window + 1 : 0;
       // where the row goes: the workspace for a piece, else the output
       const bool piece = w.part >= 0;
-      float* const part = p.parts + (size_t)max(w.part, 0) * C::PartFloats + 128 * wg + tr;
+      uint32_t* const part = p.parts + (size_t)(2 * max(w.part, 0) + rank) * C::PartWords + 128 * wg + tr;
       uint16_t* const out = static_cast<uint16_t*>(p.a.out) + (int64_t)(w.q0 + tok) * p.a.out_token_stride +
                             (int64_t)(w.h * p.G + row - tok * p.G) * p.a.out_head_stride;
       const int t0 = have ? w.t0 : 0, t1 = have ? w.t1 : 0;
@@ -718,16 +691,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (!ok) break;
       tc_fence_after_sync();
       if (piece) {
+        float amax = 0.0f;
 #pragma unroll 1
         for (int c = 0; c < kD; c += 32) {
           uint32_t v[32];
           tmem_ld32(tO + c, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) part[(c + i) * kCtaRows] = __uint_as_float(v[i]);
+          for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(__uint_as_float(v[i])));
         }
-        part[kD * kCtaRows] = M;
-        part[(kD + 1) * kCtaRows] = l;
+        const int e = amax > 0.0f && amax < INFINITY ? max((int)(__float_as_uint(amax) >> 23) - 127, -100) : 14;
+        const float mul = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+#pragma unroll 1
+        for (int c = 0; c < kD; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(tO + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            part[(c + i) / 2 * kCtaRows] = pack_f16x2(__uint_as_float(v[i]) * mul, __uint_as_float(v[i + 1]) * mul);
+        }
+        part[kD / 2 * kCtaRows] = __float_as_uint(M);
+        part[(kD / 2 + 1) * kCtaRows] = __float_as_uint(l);
+        part[(kD / 2 + 2) * kCtaRows] = (uint32_t)(127 - 14 + e) << 23;
       } else {
         // 64 values at a time through shared memory, so that the stores cover whole lines of a row
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
@@ -801,41 +787,64 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
 }
 
-// Adds the pieces of the blocks that the last round cut.  blockIdx.x: block of that round, blockIdx.y:
+// Adds the parts of the items that were cut.  blockIdx.x: item of the last round, blockIdx.y:
 // 16 values, blockIdx.z: CTA of the pair; thread = row.
 template <int kD>
-__global__ void __launch_bounds__(kCtaRows) k_prompt_join(const PromptParams p, int pairs) {
+__global__ void __launch_bounds__(kCtaRows) k_prompt_join(const PromptParams p) {
   using C = PromptCfg<kD>;
   grid_dep_wait();
-  const int items = *p.plan.count * p.a.Hkv, rounds = items / pairs, rest = items - rounds * pairs;
-  const int x = blockIdx.x;
-  if (x >= rest) return;
-  const int item = rounds * pairs + x, f = pairs / rest;
-  const int2 e = p.plan.list[item / p.a.Hkv];
+  const PromptTail& tail = *p.plan.tail;
+  if (!tail.pour || blockIdx.x >= tail.rest) return;
+  const long long item = (long long)tail.rounds * p.plan.pairs + blockIdx.x;
+  const int4 e = p.plan.list[item / p.a.Hkv];
+  const int h = (int)(item % p.a.Hkv);
+  // the parts' places in the order of the pairs: the first one is its pair's last piece
+  __shared__ int places[kPromptPairs], count;
+  if (threadIdx.x < 32) {
+    const int at = tail.start[blockIdx.x] + kItemStart;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < (kPromptPairs + 31) / 32; ++i) {
+      const int c = 32 * i + threadIdx.x;
+      const bool here = c < p.plan.pairs && prompt_cut(tail.bound[c] - at, e.z) < prompt_cut(tail.bound[c + 1] - at, e.z);
+      const uint32_t mask = __ballot_sync(~0u, here);
+      const int k = n + __popc(mask & ((1u << threadIdx.x) - 1));
+      if (here) places[k] = 2 * (2 * c + (k == 0 ? 1 : 0)) + blockIdx.z;
+      n += __popc(mask);
+    }
+    if (threadIdx.x == 0) count = n;
+  }
+  __syncthreads();
+  if (count == 1) return;
   PromptWork w;
   prompt_block(p.a, p.G, p.page_shift, e.x, e.y, w);
-  const int np = max(1, min(f, (w.t1 - w.t0) / kMinPieceTiles));
-  if (np == 1) return;
-  const int h = item % p.a.Hkv, row = w.row0 + kCtaRows * blockIdx.z + threadIdx.x;
+  const int row = w.row0 + kCtaRows * blockIdx.z + threadIdx.x;
   if (row >= w.rows) return;
-  // part of piece i: CTA 2 (x f + i) + rank
-  const float* parts = p.parts + (size_t)(2 * x * f + blockIdx.z) * C::PartFloats + threadIdx.x;
-  constexpr size_t kNext = 2 * (size_t)C::PartFloats;
+  auto part = [&](int i) { return p.parts + (size_t)places[i] * C::PartWords + threadIdx.x; };
   float M = -INFINITY;
-  for (int i = 0; i < np; ++i) M = fmaxf(M, parts[i * kNext + kD * kCtaRows]);
+#pragma unroll 8
+  for (int i = 0; i < count; ++i) M = fmaxf(M, __uint_as_float(part(i)[kD / 2 * kCtaRows]));
   float l = 0.0f, acc[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
   const int c0 = blockIdx.y * 16;
-  for (int i = 0; i < np; ++i) {
-    const float* o = parts + i * kNext;
-    const float m = o[kD * kCtaRows];
-    // a piece whose tokens this row does not see has an empty sum
-    if (m == -INFINITY) continue;
-    const float wgt = m == M ? 1.0f : exp2_approx(m - M);
-    l = __fmaf_rn(o[(kD + 1) * kCtaRows], wgt, l);
+#pragma unroll 2
+  for (int i = 0; i < count; ++i) {
+    const uint32_t* o = part(i);
+    const float m = __uint_as_float(o[kD / 2 * kCtaRows]), lp = __uint_as_float(o[(kD / 2 + 1) * kCtaRows]);
+    const float scale = __uint_as_float(o[(kD / 2 + 2) * kCtaRows]);
+    uint32_t x[8];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) acc[j] = __fmaf_rn(o[(c0 + j) * kCtaRows], wgt, acc[j]);
+    for (int j = 0; j < 8; ++j) x[j] = o[(c0 / 2 + j) * kCtaRows];
+    if (m == -INFINITY) continue;    // a part whose tokens this row does not see has an empty sum
+    const float wgt = m == M ? 1.0f : exp2_approx(m - M), f = wgt * scale;
+    l = __fmaf_rn(lp, wgt, l);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
+      acc[2 * j] = __fmaf_rn(v.x, f, acc[2 * j]);
+      acc[2 * j + 1] = __fmaf_rn(v.y, f, acc[2 * j + 1]);
+    }
   }
   const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
   const int i = row / p.G;
@@ -857,7 +866,7 @@ bool prompt_fits(int T, int G, int B) {
   return (long long)T * G / kBlockRows + B <= kMaxBlocks;
 }
 
-size_t prompt_workspace_bytes(int D) { return kPlanBytes + (size_t)kPromptCtas * kCtaRows * (D + 2) * 4; }
+size_t prompt_workspace_bytes(int D) { return kPlanBytes + (size_t)2 * kPromptCtas * kCtaRows * (D / 2 + 3) * 4; }
 
 template <int kD>
 static cudaError_t launch_prompt(const moe_kv_attention_args& a, int* status, void* space,
@@ -877,9 +886,9 @@ static cudaError_t launch_prompt(const moe_kv_attention_args& a, int* status, vo
   p.page_shift = __builtin_ctz((unsigned)a.page_size);
   p.magic = p.G == 1 ? 0 : (uint32_t)(((1ull << 32) + p.G - 1) / p.G);
   p.plan = prompt_plan_at(space);
-  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(space) + kPlanBytes);
+  p.parts = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(space) + kPlanBytes);
   p.status = status;
-  const int pairs = std::min(kPromptCtas, sm_count()) / 2;
+  const int pairs = p.plan.pairs;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kPromptThreads);
@@ -895,7 +904,7 @@ static cudaError_t launch_prompt(const moe_kv_attention_args& a, int* status, vo
   cfg.numAttrs = 2;
   err = cudaLaunchKernelEx(&cfg, k_attn_prompt<kD>, tmK, tmV, p);
   if (err != cudaSuccess) return err;
-  return launch_pdl(k_prompt_join<kD>, dim3(pairs, kD / 16, 2), dim3(kCtaRows), 0, s, p, pairs);
+  return launch_pdl(k_prompt_join<kD>, dim3(pairs, kD / 16, 2), dim3(kCtaRows), 0, s, p);
 }
 
 cudaError_t launch_attn_prompt(const moe_kv_attention_args& a, int* status, void* space, cudaStream_t s) {

@@ -448,6 +448,24 @@ def test_attention_long_items_are_joined_in_two_steps(Hq, Hkv, D, ctx, add):
     assert torch.equal(check_attention(*case, max_q=max(add), ws=ws), first)
 
 
+@pytest.mark.parametrize("D,P,Hq,Hkv,ctx,add,window", [
+    (128, 64, 8, 2, [3000, 0, 40], [700, 130, 1], 0),      # fewer blocks than pairs, each over several of them
+    (64, 16, 64, 8, [2000], [1000], 0),                    # one round of whole blocks, a last one poured over pairs
+    (128, 32, 64, 8, [1800, 100], [700, 450], 0),          # unequal loads before the last round
+    (64, 32, 3, 3, [6000, 5000], [300, 200], 0),           # parts that some rows do not see
+    (128, 16, 4, 1, [0] * 90 + [1900], [140] * 90 + [200], 300),   # short blocks, odd rounds, not poured
+    (128, 128, 40, 8, [0], [900], 0),
+])
+def test_attention_prompts_shared_by_pairs(D, P, Hq, Hkv, ctx, add, window):
+    rng = np.random.default_rng(P + Hq)
+    case = attention_case(rng, ctx, add, P, Hq, Hkv, D, extra_tokens=3)
+    first = check_attention(*case, max_q=max(add), window=window).clone()
+    again = moe.kv_attention(case[0], case[2], case[5].block_table, case[5].kv_len, case[5].tok_start,
+                             moe.alloc_kv_attention_workspace(Hq, Hkv, D, max(add)), max_q=max(add), window=window)
+    n = sum(add)
+    assert torch.equal(again[:n], first[:n])
+
+
 # ------------------------------------------------------------------------------- the pieces together
 def test_paged_attention_over_steps():
     """PagedAttention over steps that add, finish, refill and roll back requests, on two layers: every
