@@ -2,7 +2,7 @@
 //
 // Every live byte of the cache is read once and costs a handful of operations, so HBM is the bound
 // (256 bytes per token and head at D = 128).  The tokens sit on the MMA's M side and the query rows
-// (tokens of the request x heads that share the key/value head, padded to 16, 32 or 64) on its N
+// (tokens of the request x heads that share the key/value head, padded to 8, 16, 32 or 64) on its N
 // side, so that one pass over a 128-token tile serves all rows, and the E4M3 codes go from the cache
 // to the tensor cores as they are:
 //   S^T[token][row] = K[token][:] . Q[row][:]          A = K tile, K-major
@@ -17,12 +17,18 @@
 // its start and end cost, and one unit per 128-token tile; CTA c takes the tiles that lie in the c-th of
 // equal shares of the flattened list.  A CTA that holds part of an item leaves its sums, maximum and
 // unscaled output in the workspace; the CTA that arrives last adds the parts, in CTA order, so results do
-// not depend on timing.
+// not depend on timing.  Where an item has many parts the last of every kJoinGroup CTAs adds theirs first
+// (128k tokens on one head: 102 us in one step, 20 us in two).
 //   warp 0      producer: lane i fetches page i of the tile (TMA), its scales and the tile's bounds
 //   warp 1      MMA issuer
-//   warps 2..   one warpgroup per 16 rows: thread = token for the scores, = d for the output
+//   warps 2..   one warpgroup per 8 or 16 rows: thread = token for the scores, = d for the output
 // The maximum that scores are taken relative to moves only when a score passes it by 8 x (2^3): then
 // all threads of the warpgroup reduce the tile's maximum and rescale, else a vote is all it costs.
+//
+// 128 requests of 8k to 16k tokens, 32 / 8 heads of 128: 447 us, 6.85 TB/s, at the measured copy rate (6.77).
+// One of 128k: 53 us, 5.1 TB/s; of 4k: 11 us, of which start and join are 9.  61 of 6 to 8k tokens, 40 / 8
+// heads: 38 us, 4.0 TB/s.  Heads of 64: 5.1 TB/s at best, a tile's chain of scores, softmax and product
+// takes longer than its bytes (three CTAs an SM instead of two: registers spill, 102 -> 108 us).
 #include <algorithm>
 
 #include "kv_plan.cuh"
@@ -41,22 +47,24 @@ constexpr float kNoScore = -3e38f;         // running maximum before the first t
 
 template <int kD, int kNR>
 struct FewCfg {
-  static constexpr int WGs = kNR / 16;
+  static constexpr int Rows = kNR < 16 ? kNR : 16;          // of a warpgroup
+  static constexpr int WGs = kNR / Rows;
   static constexpr int Threads = 64 + 128 * WGs;
   static constexpr int HalfBytes = kTile * kD;              // K or V of a tile
   static constexpr int StageBytes = 2 * HalfBytes;
-  static constexpr int CtasPerSm = kNR == 16 ? 2 : 1;
-  static constexpr int Stages = (kNR == 16 ? 3 : 5) * (128 / kD);
+  static constexpr int CtasPerSm = kNR <= 16 ? 2 : 1;
+  static constexpr int Stages = (kNR <= 16 ? 3 : 5) * (128 / kD);
   static constexpr int QBytes = 2 * kNR * kD;
-  static constexpr int PBytes = 3 * kNR * kTile;
+  static constexpr int PPieces = kNR < 16 ? 2 : 3 * kNR / 16;   // of 16 columns: 8 rows' three terms fill 1.5
+  static constexpr int PBytes = PPieces * 16 * kTile;
   static constexpr int SCols = 2 * kNR;                     // per score buffer, two of them
   static constexpr int OCol = 2 * SCols;
-  static constexpr int TmemCols = kNR == 16 ? 128 : kNR == 32 ? 256 : 512;
-  static constexpr int LdCols = kNR == 64 ? 8 : 16;         // 64 rows: 96 registers a thread
+  static constexpr int TmemCols = kNR == 8 ? 64 : kNR == 16 ? 128 : kNR == 32 ? 256 : 512;
+  static constexpr int LdCols = kNR == 64 || kNR == 8 ? 8 : 16;   // 64 rows: 96 registers a thread
   static constexpr int SlotBytes = 128;
   static constexpr int CtrlBytes = 1024 + Stages * SlotBytes + WGs * 5 * 16 * 4;
   static constexpr int Smem = 1024 + Stages * StageBytes + QBytes + PBytes + CtrlBytes;
-  static_assert(OCol + 3 * kNR <= TmemCols, "tensor memory");
+  static_assert(OCol + 16 * PPieces <= TmemCols, "tensor memory");
   static_assert(CtasPerSm * (Smem + 1024) <= 228 * 1024, "shared memory");
 };
 
@@ -127,22 +135,24 @@ struct FewWalk {
   }
 };
 
-// 16 values per lane -> the reduction over the warp of value r = lane >> 1 (both lanes of a pair).
-template <bool kMax>
-__device__ __forceinline__ float warp_reduce16(float (&v)[16], int lane) {
+// kN values per lane (8 or 16) -> the reduction over the warp of value r = lane / (32 / kN).
+template <bool kMax, int kN>
+__device__ __forceinline__ float warp_reduce_rows(float (&v)[kN], int lane) {
+  auto both = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
 #pragma unroll
-  for (int half = 8; half >= 1; half >>= 1) {
-    const int d = 2 * half;
+  for (int half = kN / 2; half >= 1; half >>= 1) {
+    const int d = half * (32 / kN);
     const bool up = lane & d;
 #pragma unroll
     for (int i = 0; i < half; ++i) {
       const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
-      const float got = __shfl_xor_sync(~0u, send, d);
-      v[i] = kMax ? fmaxf(keep, got) : keep + got;
+      v[i] = both(keep, __shfl_xor_sync(~0u, send, d));
     }
   }
-  const float got = __shfl_xor_sync(~0u, v[0], 1);
-  return kMax ? fmaxf(v[0], got) : v[0] + got;
+  float r = v[0];
+#pragma unroll
+  for (int d = 16 / kN; d >= 1; d >>= 1) r = both(r, __shfl_xor_sync(~0u, r, d));
+  return r;
 }
 
 // kN consecutive 32-bit tensor-memory columns of this warp's lanes (8 or 16).
@@ -172,10 +182,11 @@ __device__ __forceinline__ uint32_t take_term(uint32_t& h2) {
 }
 
 // P lies token by token (MN-major B): 8 tokens x 16 rows of one term are 128 contiguous bytes, the
-// terms' and warpgroups' 16-row pieces follow each other, then the next 8 tokens.
+// terms' and warpgroups' 16-row pieces follow each other, then the next 8 tokens.  With 8 rows the first
+// piece holds two terms, the second one and zeros.
 template <int kNR>
 __device__ __forceinline__ uint64_t p_desc(uint32_t saddr) {
-  constexpr uint32_t kPieces = 3 * kNR / 16;
+  constexpr uint32_t kPieces = FewCfg<128, kNR>::PPieces;
   uint64_t d = 0;
   d |= (uint64_t)((saddr & 0x3FFFF) >> 4);
   d |= (uint64_t)((kPieces * 128) >> 4) << 16;   // between groups of 8 tokens
@@ -529,7 +540,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       // ------------------------------------------------------------------------- MMA
       {
         constexpr uint32_t kIdescS = make_idesc_e4m3(kTile, 2 * kNR);
-        constexpr uint32_t kIdescO = make_idesc_e4m3(kD, 3 * kNR) | (3u << 15);   // both MN-major
+        constexpr uint32_t kIdescO = make_idesc_e4m3(kD, 16 * C::PPieces) | (3u << 15);   // both MN-major
         const uint64_t qd = rows_desc<kD>(sQ), pd = p_desc<kNR>(sP);
         int segs = 0;
         const bool ok = true;
@@ -561,7 +572,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           const uint32_t sv = sbase + s * C::StageBytes + C::HalfBytes;
 #pragma unroll
           for (int k = 0; k < kTile / 32; ++k)
-            mma_f8_warp(tmem + C::OCol, rows_desc<kD>(sv + k * 32 * kD), pd + k * (32 * 3 * kNR / 16), kIdescO, k > 0);
+            mma_f8_warp(tmem + C::OCol, rows_desc<kD>(sv + k * 32 * kD), pd + k * (32 * C::PPieces), kIdescO, k > 0);
           mma_commit_warp(ofull);
           mma_commit_warp(empty(s));
           if (lane == 0) *mma_done = it + 1;
@@ -582,8 +593,11 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       float* wred = red + wg * 80;                      // [4 warps][16 rows], for reductions
       float* wqs = wred + 64;                           // [16 rows] value of a code of Q
       const int r0 = wg * 16;
-      float m[16];
-      f32x2 l[8], acc[8];                               // two rows each
+      constexpr int kR = C::Rows;
+      constexpr uint32_t kAllRows = (1u << kR) - 1;
+      constexpr int kRowLanes = 32 / kR;                // lanes that share a row's reduction
+      float m[kR];
+      f32x2 l[kR / 2], acc[kR / 2];                     // two rows each
       float vref_prev = 0.0f;
       // A wait that runs out only marks the thread: the warpgroup leaves together, at the next vote,
       // so no barrier is left waiting.
@@ -597,7 +611,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         const float f = vref_prev * (1.0f / kPScale);
         const f32x2 f2 = pack2(f, f), step = pack2(1.0f / kTermStep, 1.0f / kTermStep);
 #pragma unroll
-        for (int r0s = 0; r0s < 16; r0s += C::LdCols) {
+        for (int r0s = 0; r0s < kR; r0s += C::LdCols) {
           uint32_t t[3][C::LdCols];
           const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + C::OCol + r0 + r0s;
 #pragma unroll
@@ -617,55 +631,57 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       // The scores of the segment before are done: this warpgroup has read them.
       auto load_q = [&](int rows, int q0, int head) {
         constexpr int kV = kD / 8;
-        const int r = r0 + (wt >> 3), c = wt & 7;
-        float x[kV];
+        if (wt < 8 * kR) {
+          const int r = r0 + (wt >> 3), c = wt & 7;
+          float x[kV];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) x[i] = 0.0f;
-        if (r < rows) {
-          const int i = r / p.G;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              static_cast<const uint16_t*>(p.a.q) + (int64_t)(q0 + i) * p.a.q_token_stride +
-              (int64_t)(head * p.G + r - i * p.G) * p.a.q_head_stride + c * kV);
+          for (int i = 0; i < kV; ++i) x[i] = 0.0f;
+          if (r < rows) {
+            const int i = r / p.G;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                static_cast<const uint16_t*>(p.a.q) + (int64_t)(q0 + i) * p.a.q_token_stride +
+                (int64_t)(head * p.G + r - i * p.G) * p.a.q_head_stride + c * kV);
 #pragma unroll
-          for (int v = 0; v < kV / 8; ++v) {
-            const uint4 w = src[v];
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            for (int v = 0; v < kV / 8; ++v) {
+              const uint4 w = src[v];
+              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              x[8 * v + 2 * j] = __uint_as_float(u[j] << 16);
-              x[8 * v + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+              for (int j = 0; j < 4; ++j) {
+                x[8 * v + 2 * j] = __uint_as_float(u[j] << 16);
+                x[8 * v + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+              }
             }
           }
-        }
-        float amax = 0.0f;
+          float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) amax = fmaxf(amax, fabsf(x[i]));
+          for (int i = 0; i < kV; ++i) amax = fmaxf(amax, fabsf(x[i]));
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-        // amax x mul in [128, 256)
-        const int e = amax > 0.0f ? max((int)(__float_as_uint(amax) >> 23) - 127, -100) : 0;
-        const float mul = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-        uint32_t t1[kV / 4], t2[kV / 4];
+          for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+          // amax x mul in [128, 256)
+          const int e = amax > 0.0f ? max((int)(__float_as_uint(amax) >> 23) - 127, -100) : 0;
+          const float mul = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+          uint32_t t1[kV / 4], t2[kV / 4];
 #pragma unroll
-        for (int i = 0; i < kV / 4; ++i) {
-          t1[i] = t2[i] = 0;
+          for (int i = 0; i < kV / 4; ++i) {
+            t1[i] = t2[i] = 0;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float a = x[4 * i + 2 * j] * mul, b = x[4 * i + 2 * j + 1] * mul;
-            const uint32_t code = cvt_e4m3x2(a, b);
-            float fa, fb;
-            e4m3x2_to_f32(code, fa, fb);
-            t1[i] |= code << (16 * j);
-            t2[i] |= cvt_e4m3x2((a - fa) * kTermStep, (b - fb) * kTermStep) << (16 * j);
+            for (int j = 0; j < 2; ++j) {
+              const float a = x[4 * i + 2 * j] * mul, b = x[4 * i + 2 * j + 1] * mul;
+              const uint32_t code = cvt_e4m3x2(a, b);
+              float fa, fb;
+              e4m3x2_to_f32(code, fa, fb);
+              t1[i] |= code << (16 * j);
+              t2[i] |= cvt_e4m3x2((a - fa) * kTermStep, (b - fb) * kTermStep) << (16 * j);
+            }
           }
-        }
-        uint8_t* qb = smem + C::Stages * C::StageBytes;
+          uint8_t* qb = smem + C::Stages * C::StageBytes;
 #pragma unroll
-        for (int i = 0; i < kV / 4; i += 2) {
-          *reinterpret_cast<uint2*>(qb + swz<kD>(r, c * kV + 4 * i)) = make_uint2(t1[i], t1[i + 1]);
-          *reinterpret_cast<uint2*>(qb + swz<kD>(kNR + r, c * kV + 4 * i)) = make_uint2(t2[i], t2[i + 1]);
+          for (int i = 0; i < kV / 4; i += 2) {
+            *reinterpret_cast<uint2*>(qb + swz<kD>(r, c * kV + 4 * i)) = make_uint2(t1[i], t1[i + 1]);
+            *reinterpret_cast<uint2*>(qb + swz<kD>(kNR + r, c * kV + 4 * i)) = make_uint2(t2[i], t2[i + 1]);
+          }
+          if (c == 0) wqs[wt >> 3] = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
         }
-        if (c == 0) wqs[wt >> 3] = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
         fence_proxy_async_smem();
         named_barrier_sync(1 + wg, 128);
         if (lane == 0) mbar_arrive(qfull);
@@ -680,9 +696,9 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         const int rows = bad ? 0 : slot.rows, pos0 = slot.pos0, q0 = slot.q0, head = slot.head;
         if (begin) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) m[i] = kNoScore;
+          for (int i = 0; i < kR; ++i) m[i] = kNoScore;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) l[i] = acc[i] = 0ull;
+          for (int i = 0; i < kR / 2; ++i) l[i] = acc[i] = 0ull;
         }
         // scores of this thread's token
         const int page = tl >> p.page_shift;
@@ -690,20 +706,20 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         const int j = slot.token0 + tl;
         const bool edge = slot.token0 < slot.lo || slot.token0 + kTile > slot.hi;
         // rows [from, to) of the warpgroup see the token; rows past the live ones may see anything
-        int from = max(j - pos0, 0) * p.G, to = 16 + r0;
+        int from = max(j - pos0, 0) * p.G, to = kR + r0;
         if (p.a.window > 0)
           to = min(to, j - pos0 + p.a.window > 0 ? min(j - pos0 + p.a.window, 64) * p.G : 0);
         if (j >= slot.hi || j < slot.lo) to = 0;
-        from = min(max(from - r0, 0), 16);
-        to = min(max(to - r0, 0), 16);
+        from = min(max(from - r0, 0), kR);
+        to = min(max(to - r0, 0), kR);
         const uint32_t seen = to > from ? ((1u << to) - (1u << from)) : 0u;
         if (!bounded_wait(sfull(it & 1), (it >> 1) & 1, abort_flag, status)) bad = true;
         tc_fence_after_sync();
-        float sc[16];
+        float sc[kR];
         {
           const f32x2 step = pack2(1.0f / kTermStep, 1.0f / kTermStep), kf2 = pack2(kf, kf);
 #pragma unroll
-          for (int r0s = 0; r0s < 16; r0s += C::LdCols) {
+          for (int r0s = 0; r0s < kR; r0s += C::LdCols) {
             uint32_t t[C::LdCols], t2[C::LdCols];
             const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (it & 1) * C::SCols + r0 + r0s;
             tmem_ldn<C::LdCols>(at, t);
@@ -723,28 +739,28 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
             }
           }
           tc_fence_before_sync();
-          if (seen != 0xFFFFu) {
+          if (seen != kAllRows) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
+            for (int r = 0; r < kR; ++r)
               if (!((seen >> r) & 1)) sc[r] = -INFINITY;
           }
         }
         bool grow = false;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) grow |= sc[r] > m[r] + kGrow;
+        for (int r = 0; r < kR; ++r) grow |= sc[r] > m[r] + kGrow;
         if (vote_any<128>(1 + wg, grow || bad)) {
           if (vote_any<128>(1 + wg, bad)) break;
           // the maximum of some row moved: bring what is outstanding in, then rescale
           if (pending) add_output(it - 1);
           pending = false;
-          float v[16];
+          float v[kR];
 #pragma unroll
-          for (int r = 0; r < 16; ++r) v[r] = sc[r];
-          const float top = warp_reduce16<true>(v, lane);
-          if (!(lane & 1)) wred[q * 16 + (lane >> 1)] = top;
+          for (int r = 0; r < kR; ++r) v[r] = sc[r];
+          const float top = warp_reduce_rows<true, kR>(v, lane);
+          if (!(lane & (kRowLanes - 1))) wred[q * 16 + lane / kRowLanes] = top;
           named_barrier_sync(1 + wg, 128);
 #pragma unroll
-          for (int r = 0; r < 16; r += 2) {
+          for (int r = 0; r < kR; r += 2) {
             float alpha[2];
 #pragma unroll
             for (int i = r; i < r + 2; ++i) {
@@ -759,9 +775,9 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         }
         if (pending) add_output(it - 1);
         // probabilities, rounded to FP16 (11 bits, down to 2^-29), then three E4M3 terms each
-        uint32_t term[3][4];
+        uint32_t term[3][kR / 4];
 #pragma unroll
-        for (int r = 0; r < 16; r += 2) {
+        for (int r = 0; r < kR; r += 2) {
           float p0, p1;
           unpack2(add2(pack2(sc[r], sc[r + 1]), pack2(-m[r], -m[r + 1])), p0, p1);
           const f32x2 pr = pack2(exp2_approx(p0), exp2_approx(p1));
@@ -775,11 +791,16 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
             else term[k][r / 4] = code;
           }
         }
+        uint8_t* pt = smem + (sP - sbase) + (tl >> 3) * (C::PPieces * 128) + (tl & 7) * 16;
+        if constexpr (kR == 8) {
+          *reinterpret_cast<uint4*>(pt) = make_uint4(term[0][0], term[0][1], term[1][0], term[1][1]);
+          *reinterpret_cast<uint4*>(pt + 128) = make_uint4(term[2][0], term[2][1], 0, 0);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
-          *reinterpret_cast<uint4*>(smem + (sP - sbase) + (tl >> 3) * (3 * kNR * 8) +
-                                    (k * C::WGs + wg) * 128 + (tl & 7) * 16) =
-              make_uint4(term[k][0], term[k][1], term[k][2], term[k][3]);
+          for (int k = 0; k < 3; ++k)
+            *reinterpret_cast<uint4*>(pt + (k * C::WGs + wg) * 128) =
+                make_uint4(term[k][0], term[k][1], term[k][kR / 4 - 2], term[k][kR / 4 - 1]);
+        }
         if (edge && wg == 0) {
           // V rows that no query row sees may hold anything: 0 x NaN would spread
           if (!bounded_wait(vfull(s), (it / C::Stages) & 1, abort_flag, status)) bad = true;
@@ -806,17 +827,17 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           }
           add_output(it);
           pending = false;
-          float lr[16], ar[16];
+          float lr[kR], ar[kR];
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
+          for (int r = 0; r < kR / 2; ++r) {
             unpack2(l[r], lr[2 * r], lr[2 * r + 1]);
             unpack2(acc[r], ar[2 * r], ar[2 * r + 1]);
           }
-          const float sum = warp_reduce16<false>(lr, lane);
-          if (!(lane & 1)) wred[q * 16 + (lane >> 1)] = sum;
+          const float sum = warp_reduce_rows<false, kR>(lr, lane);
+          if (!(lane & (kRowLanes - 1))) wred[q * 16 + lane / kRowLanes] = sum;
           named_barrier_sync(1 + wg, 128);
-          // lane r and r + 16 know row r's sum and place; the others ask them
-          const int mr = lane & 15, my_row = r0 + mr;
+          // every kR-th lane from r on knows row r's sum and place; the others ask them
+          const int mr = lane & (kR - 1), my_row = r0 + mr;
           const float lsum = (wred[mr] + wred[16 + mr]) + (wred[32 + mr] + wred[48 + mr]);
           if (part < 0) {
             const float inv = lsum > 0.0f || lsum != lsum ? 1.0f / lsum : 0.0f;
@@ -824,7 +845,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
             const long long at = (long long)(q0 + i) * p.a.out_token_stride +
                                  (long long)(head * p.G + my_row - i * p.G) * p.a.out_head_stride;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
+            for (int r = 0; r < kR; ++r) {
               if (r0 + r >= rows) break;
               const float f = __shfl_sync(~0u, inv, r);
               const long long o = __shfl_sync(~0u, at, r);
@@ -834,16 +855,16 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
             float* o = p.parts + (size_t)part * (kNR * (kD + 2));
             float mm = 0.0f;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
+            for (int r = 0; r < kR; ++r) {
               if (mr == r) mm = m[r];
               if (r0 + r < rows && holds_d) o[(r0 + r) * kD + d] = ar[r];
             }
-            if (wt < 16 && my_row < rows)
+            if (wt < kR && my_row < rows)
               *reinterpret_cast<float2*>(o + kNR * kD + 2 * my_row) = make_float2(mm, lsum);
           }
           if (part >= 0) {
             // the last of a group of CTAs to get here adds the group's parts, the last of the groups theirs
-            const int row1 = min(rows, r0 + 16), jw = wt >> 5;
+            const int row1 = min(rows, r0 + kR), jw = wt >> 5;
             JoinSet set;
             set.first = first_part;
             set.rest = 2 * first_cta;
@@ -918,14 +939,18 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
 }
 
 // ------------------------------------------------------------------------------------ launch
-// Rows per item of a call: tokens of a request x heads that share a key/value head, 16, 32 or 64.
+// Rows per item of a call: tokens of a request x heads that share a key/value head, 8, 16, 32 or 64.  Rows
+// cost softmax time whether they are live or not, so the fewest that hold them win: 64 x 4000 tokens, 4 rows
+// live, 8 / 16 / 32 / 64 rows: 89 / 90 / 120 / 235 us; 40 x 4000, 16 live: 42 / 51 / 89 us from 16 on.
+// More than 64 rows are the prompt kernel's; up to 64 this one is faster (32 rows, 32 x 4000: 44 against
+// 114 us; 64 rows, 32 x 8000: 130 against 198 us), and at 72 and 96 the prompt kernel costs what it does at 64.
 int few_rows(int G, int max_q) {
   const long long r = (long long)G * max_q;
   const long long rows = r <= 64 ? r : G;   // prompts: the single tokens among them still come here
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-static int few_ctas(int nr) { return nr == 16 ? 304 : 152; }   // at most; 152 SMs
+static int few_ctas(int nr) { return nr <= 16 ? 304 : 152; }   // at most; 152 SMs
 
 size_t few_workspace_bytes(int D, int nr) {
   const int ctas = few_ctas(nr);
@@ -959,12 +984,18 @@ static cudaError_t launch(const moe_kv_attention_args& a, void* workspace, void*
   return launch_pdl(k_attn_few<kD, kNR>, dim3(ctas), dim3(C::Threads), C::Smem, s, tmK, tmV, p);
 }
 
+template <int kD>
+static cudaError_t launch_rows(const moe_kv_attention_args& a, int nr, void* workspace, void* plan, cudaStream_t s) {
+  switch (nr) {
+    case 8: return launch<kD, 8>(a, workspace, plan, s);
+    case 16: return launch<kD, 16>(a, workspace, plan, s);
+    case 32: return launch<kD, 32>(a, workspace, plan, s);
+    default: return launch<kD, 64>(a, workspace, plan, s);
+  }
+}
+
 cudaError_t launch_attn_few(const moe_kv_attention_args& a, int nr, void* workspace, void* plan, cudaStream_t s) {
-  if (a.D == 128)
-    return nr == 16 ? launch<128, 16>(a, workspace, plan, s)
-           : nr == 32 ? launch<128, 32>(a, workspace, plan, s) : launch<128, 64>(a, workspace, plan, s);
-  return nr == 16 ? launch<64, 16>(a, workspace, plan, s)
-         : nr == 32 ? launch<64, 32>(a, workspace, plan, s) : launch<64, 64>(a, workspace, plan, s);
+  return a.D == 128 ? launch_rows<128>(a, nr, workspace, plan, s) : launch_rows<64>(a, nr, workspace, plan, s);
 }
 
 }  // namespace moe
