@@ -904,6 +904,10 @@ static cudaError_t launch_prompt(const moe_kv_attention_args& a, int* status, vo
   cfg.numAttrs = 2;
   err = cudaLaunchKernelEx(&cfg, k_attn_prompt<kD>, tmK, tmV, p);
   if (err != cudaSuccess) return err;
+  // nothing is cut where no block can see enough tiles: one launch less (3 x 104 tokens: 15.6 -> 14.6 us)
+  long long tiles = ((long long)a.max_pages * a.page_size + kTile - 1) / kTile;
+  if (a.window > 0) tiles = std::min(tiles, ((long long)a.window + kBlockRows / p.G + 1) / kTile + 2);
+  if (tiles < kCutTiles) return cudaSuccess;
   return launch_pdl(k_prompt_join<kD>, dim3(pairs, kD / 16, 2), dim3(kCtaRows), 0, s, p);
 }
 
