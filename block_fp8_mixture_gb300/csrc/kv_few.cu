@@ -25,9 +25,9 @@
 // The maximum that scores are taken relative to moves only when a score passes it by 8 x (2^3): then
 // all threads of the warpgroup reduce the tile's maximum and rescale, else a vote is all it costs.
 //
-// 128 requests of 8k to 16k tokens, 32 / 8 heads of 128: 447 us, 6.85 TB/s, at the measured copy rate (6.77).
-// One of 128k: 53 us, 5.1 TB/s; of 4k: 11 us, of which start and join are 9.  61 of 6 to 8k tokens, 40 / 8
-// heads: 38 us, 4.0 TB/s.  Heads of 64: 5.1 TB/s at best, a tile's chain of scores, softmax and product
+// 128 requests of 8k to 16k tokens, 64 / 8 heads of 128: 447 us, 6.85 TB/s, at the measured copy rate (6.77).
+// 32 / 8 heads, one request of 128k: 53 us, 5.1 TB/s; of 4k: 11 us, of which start and join are 9.  61 of 6
+// to 8190 tokens, 40 / 8 heads: 38 us, 4.0 TB/s.  Heads of 64: 5.1 TB/s at best, a tile's chain of scores, softmax and product
 // takes longer than its bytes (three CTAs an SM instead of two: registers spill, 102 -> 108 us).
 #include <algorithm>
 

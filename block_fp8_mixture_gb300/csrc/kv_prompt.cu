@@ -24,10 +24,12 @@
 // Work: rounds over the blocks, longest first, and a last one whose tiles are poured over the pairs up to
 // a common level (kv_plan.cuh).  Blocks that this cuts along the cache k_prompt_join adds up, in order.
 //
-// 4096 tokens after 28000, 32 / 8 heads of 128: 1.375 ms, 1.47 PFLOP/s, 78% of the measured 16-bit rate
-// (one CTA per block of 256 rows: 1.59 ms; V read past shared memory: 1.72 ms; two threads a row: 1.52 ms;
-// an issuing warp per tile of rows: 1.85 ms).  A step of 512 rows x 128 tokens takes about 3300 cycles, of
-// which the products need 2050: what is left is the chain score -> softmax -> product of each tile.
+// 4096 tokens after 28000, 32 / 8 heads of 128: 1.29 ms, 1.56 PFLOP/s, 83% of the measured 16-bit rate.  At
+// 1.42 ms the other layouts took: one CTA per block of 256 rows 1.59 ms; V read past shared memory 1.72 ms;
+// two threads a row 1.52 ms; an issuing warp per tile of rows 1.85 ms.  A step of 512 rows x 128 tokens takes
+// about 3300 cycles, of which the products need 2050: what is left is the chain score -> softmax -> product
+// of each tile.  Five prompts of 300 to 4000 tokens: 174 us, 1.04 PFLOP/s, the start and end of each block
+// being about 2.5 steps.
 #include <cuda_fp16.h>
 
 #include <algorithm>

@@ -136,10 +136,17 @@ moe_status moe_rope_append(const moe_rope_append_args* args, moe_stream_t stream
  * mistake: their later rows are left unwritten).
  * A NaN code among the tokens that some row of the call sees may reach other rows of the same request;
  * codes outside every row's view (stale rows of the last page, other pages) never matter.
- * Supported: Hq % Hkv == 0, Hq / Hkv <= 64, sm_scale finite and > 0, 1 <= B <= 4096, max_q >= 1.
+ * Supported: 1 <= num_pages, Hq % Hkv == 0, Hq / Hkv <= 64, sm_scale finite and > 0, 1 <= B <= 4096, max_q >= 1.
  * Strides in elements, multiples of 8.
+ * Parts of a long request are kept in the workspace on the way: FP32 with few query rows, FP16 with a
+ * scale per row (and FP32 statistics) with many, which is less than the rounding of out.
+ * MOE_ERR_INVALID_ARG with num_pages 0; MOE_ERR_UNSUPPORTED_SHAPE where the work would pass 32-bit counts:
+ * T * (Hq / Hkv) / 512 + B > 65536 with more rows than 64 in a request, or
+ * Hkv * (B * max_pages * page_size / 128 + 4 * B) >= 2^31 - 2^20.
  * The workspace (256-byte aligned) starts with the int32 status word that moe_last_device_status
- * reads; the caller zeroes the workspace once after allocating it. */
+ * reads; the caller zeroes the workspace once after allocating it, and again after a call whose status
+ * is MOE_ERR_DEVICE_TIMEOUT (the status stays, and counters may be left half way).  One workspace serves
+ * one stream at a time. */
 typedef struct {
   const void* q;               /* bf16 [T, Hq, D] */
   const void* k_codes;
