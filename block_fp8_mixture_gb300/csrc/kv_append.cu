@@ -105,13 +105,11 @@ __global__ void __launch_bounds__(kWPU == 8 ? 256 : 128)
   const int chunks = a.D >> 4;                 // threads per row: 4 or 8
   const int cshift = a.D == 128 ? 3 : 2;
 
-  // cache blocks and query blocks are spread evenly over the grid: the former wait for chains of loads,
-  // the latter keep HBM busy meanwhile
-  const unsigned kv_at = min(blockIdx.x, (unsigned)kv_blocks);
+  // the cache's blocks come first: they wait for chains of loads and finish last
   const bool is_kv = blockIdx.x < (unsigned)kv_blocks;
   if (!is_kv) {                                // ---------------------------------- Q
     // a block takes one token: its cos and sin are loaded once for all heads of a thread
-    const int t = blockIdx.x - kv_at, c = threadIdx.x & (chunks - 1);
+    const int t = blockIdx.x - kv_blocks, c = threadIdx.x & (chunks - 1);
     const Chunk16 ch = chunk16(c, a.rot_dim, a.layout);
     const uint16_t* q = static_cast<const uint16_t*>(a.q) + t * a.q_token_stride;
     uint16_t* o = static_cast<uint16_t*>(a.q_out) + t * a.qo_token_stride;
@@ -150,7 +148,7 @@ __global__ void __launch_bounds__(kWPU == 8 ? 256 : 128)
   __shared__ float red[kThreads / 32];
   const int warp = threadIdx.x >> 5;
   const int ut = threadIdx.x & (32 * kWPU - 1);          // thread within the unit
-  const unsigned unit = kv_at * kUnits + warp / kWPU;
+  const unsigned unit = blockIdx.x * kUnits + warp / kWPU;
   const unsigned run = unit / (2 * a.Hkv);
   const int hv = (int)(unit - run * 2 * a.Hkv);          // head and K / V
   // whole units leave together, so the barriers below stay complete

@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
   const int cta = (int)blockIdx.x - (p.plan.list != nullptr ? 1 : 0);
   if (cta < 0) {
     grid_dep_wait();
+    grid_dep_launch_dependents();
     prompt_plan(p.a, p.plan, p.G, p.page_shift, reinterpret_cast<int*>(smem));
     return;
   }
@@ -346,6 +347,9 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
   // an exclusive sum over threads with consecutive requests each
   auto weight = [&](const FewItem& it) { return it.tiles ? (it.tiles + kItemUnits) * p.a.Hkv : 0; };
   grid_dep_wait();
+  // With prompts the next kernel's start is the call's own; else it would only be in this one's way (1 x 4k:
+  // 11.2 -> 11.6 us).
+  if (p.plan.list != nullptr) grid_dep_launch_dependents();
   const int per = (p.a.B + C::Threads - 1) / C::Threads;
   const int rb0 = threadIdx.x * per, rb1 = min(p.a.B, rb0 + per);
   int mine = 0;
