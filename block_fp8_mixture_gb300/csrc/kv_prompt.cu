@@ -24,11 +24,11 @@
 // Work: rounds over the blocks, longest first, and a last one whose tiles are poured over the pairs up to
 // a common level (kv_plan.cuh).  Blocks that this cuts along the cache k_prompt_join adds up, in order.
 //
-// 4096 tokens after 28000, 32 / 8 heads of 128: 1.29 ms, 1.56 PFLOP/s, 83% of the measured 16-bit rate.  At
+// 4096 tokens after 28000, 32 / 8 heads of 128: 1.28 ms, 1.58 PFLOP/s, 84% of the measured 16-bit rate.  At
 // 1.42 ms the other layouts took: one CTA per block of 256 rows 1.59 ms; V read past shared memory 1.72 ms;
 // two threads a row 1.52 ms; an issuing warp per tile of rows 1.85 ms.  A step of 512 rows x 128 tokens takes
 // about 3300 cycles, of which the products need 2050: what is left is the chain score -> softmax -> product
-// of each tile.  Five prompts of 300 to 4000 tokens: 174 us, 1.04 PFLOP/s, the start and end of each block
+// of each tile.  Five prompts of 300 to 4000 tokens: 173 us, 1.04 PFLOP/s, the start and end of each block
 // being about 2.5 steps.
 #include <cuda_fp16.h>
 
@@ -76,6 +76,7 @@ struct PromptParams {
   uint32_t magic;              // ceil(2^32 / G), 0 for G = 1: row / G is a multiply for row < 2^26
   uint32_t* parts;             // [2 * pairs][CTA of the pair][PartWords]
   int* status;
+  bool join;                   // k_prompt_join follows
 };
 
 __device__ __forceinline__ int token_of(const PromptParams& p, int row) {
@@ -247,7 +248,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   grid_dep_wait();
-  grid_dep_launch_dependents();
 
   // The producer looks the pieces of work up, ahead of everybody, and hands them on: the k-th, for a warp
   // of another role; false when there are no more.
@@ -263,6 +263,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
   // Tensor memory: S of row tile w (P in its first half) at 128 w, O at 256 + 128 w.
   if (warp < 4) {
+    // One idle warp triggers the join's launch, which waits for this kernel's end all the same (in every warp
+    // this costs 2% of a chunk).  Where no join follows, the caller's next kernel would only be in the way.
+    if (warp == 3 && p.join) grid_dep_launch_dependents();
     regs_down<kRegsIssue>();
     if (warp == 0) {
       // -------------------------------------------------------------------- producer
@@ -891,6 +894,10 @@ static cudaError_t launch_prompt(const moe_kv_attention_args& a, int* status, vo
   p.parts = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(space) + kPlanBytes);
   p.status = status;
   const int pairs = p.plan.pairs;
+  // nothing is cut where no block can see enough tiles: one launch less (3 x 104 tokens: 15.6 -> 13.8 us)
+  long long tiles = ((long long)a.max_pages * a.page_size + kTile - 1) / kTile;
+  if (a.window > 0) tiles = std::min(tiles, ((long long)a.window + kBlockRows / p.G + 1) / kTile + 2);
+  p.join = tiles >= kCutTiles;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kPromptThreads);
@@ -906,10 +913,7 @@ static cudaError_t launch_prompt(const moe_kv_attention_args& a, int* status, vo
   cfg.numAttrs = 2;
   err = cudaLaunchKernelEx(&cfg, k_attn_prompt<kD>, tmK, tmV, p);
   if (err != cudaSuccess) return err;
-  // nothing is cut where no block can see enough tiles: one launch less (3 x 104 tokens: 15.6 -> 14.6 us)
-  long long tiles = ((long long)a.max_pages * a.page_size + kTile - 1) / kTile;
-  if (a.window > 0) tiles = std::min(tiles, ((long long)a.window + kBlockRows / p.G + 1) / kTile + 2);
-  if (tiles < kCutTiles) return cudaSuccess;
+  if (!p.join) return cudaSuccess;
   return launch_pdl(k_prompt_join<kD>, dim3(pairs, kD / 16, 2), dim3(kCtaRows), 0, s, p);
 }
 
