@@ -22,6 +22,18 @@ static moe_status check_cache(int Hkv, int D, int page_size, int num_pages) {
 
 static bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }
 
+// The workspace: status and counters, the prompts' plan, and parts, which the two kernels need one after the other.
+struct AttentionSpace {
+  size_t plan, parts, total;
+};
+static AttentionSpace attention_space(int D, int rows, bool prompts) {
+  AttentionSpace w;
+  w.plan = few_counter_bytes(rows);
+  w.parts = w.plan + (prompts ? prompt_plan_bytes() : 0);
+  w.total = w.parts + std::max(few_parts_bytes(D, rows), prompts ? prompt_parts_bytes(D) : (size_t)0);
+  return w;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -99,8 +111,7 @@ size_t moe_kv_attention_workspace_bytes(int Hq, int Hkv, int D, int max_q) {
   if (Hq <= 0 || max_q <= 0 || check_cache(Hkv, D, 16, 0) != MOE_OK) return 0;
   if (Hq % Hkv || Hq / Hkv > kMaxGroup) return 0;
   const int G = Hq / Hkv, rows = few_rows(G, max_q);
-  const size_t few = (few_workspace_bytes(D, rows) + 255) & ~(size_t)255;
-  return (long long)G * max_q > rows ? few + prompt_workspace_bytes(D) : few;
+  return attention_space(D, rows, (long long)G * max_q > rows).total;
 }
 
 moe_status moe_kv_attention(const moe_kv_attention_args* a, void* workspace, size_t workspace_bytes,
@@ -134,11 +145,12 @@ moe_status moe_kv_attention(const moe_kv_attention_args* a, void* workspace, siz
   const int G = a->Hq / a->Hkv, rows = few_rows(G, a->max_q);
   const bool prompts = (long long)G * a->max_q > rows;   // some request may have more rows than that
   if (prompts && !prompt_fits(a->T, G, a->B)) return MOE_ERR_UNSUPPORTED_SHAPE;
-  const size_t few = (few_workspace_bytes(a->D, rows) + 255) & ~(size_t)255;
-  void* space = prompts ? static_cast<uint8_t*>(workspace) + few : nullptr;
-  cudaError_t err = launch_attn_few(c, rows, workspace, space, (cudaStream_t)stream);
+  const AttentionSpace w = attention_space(a->D, rows, prompts);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  void* plan = prompts ? ws + w.plan : nullptr;
+  cudaError_t err = launch_attn_few(c, rows, workspace, plan, ws + w.parts, (cudaStream_t)stream);
   if (err == cudaSuccess && prompts)
-    err = launch_attn_prompt(c, static_cast<int*>(workspace), space, (cudaStream_t)stream);
+    err = launch_attn_prompt(c, static_cast<int*>(workspace), plan, ws + w.parts, (cudaStream_t)stream);
   return launched(err);
 }
 

@@ -956,13 +956,12 @@ int few_rows(int G, int max_q) {
 
 static int few_ctas(int nr) { return nr <= 16 ? 304 : 152; }   // at most; 152 SMs
 
-size_t few_workspace_bytes(int D, int nr) {
-  const int ctas = few_ctas(nr);
-  return 256 + (size_t)ctas * 32 + (size_t)2 * ctas * nr * (D + 2) * 4;
-}
+size_t few_counter_bytes(int nr) { return (256 + (size_t)few_ctas(nr) * 32 + 255) & ~(size_t)255; }
+
+size_t few_parts_bytes(int D, int nr) { return (size_t)2 * few_ctas(nr) * nr * (D + 2) * 4; }
 
 template <int kD, int kNR>
-static cudaError_t launch(const moe_kv_attention_args& a, void* workspace, void* plan, cudaStream_t s) {
+static cudaError_t launch(const moe_kv_attention_args& a, void* workspace, void* plan, void* parts, cudaStream_t s) {
   using C = FewCfg<kD, kNR>;
   CUtensorMap tmK, tmV;
   if (!cache_map(&tmK, a.k_codes, kD, a.page_size, a.Hkv, a.num_pages, a.page_size, kD) ||
@@ -979,7 +978,7 @@ static cudaError_t launch(const moe_kv_attention_args& a, void* workspace, void*
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.status = reinterpret_cast<int*>(ws);
   p.arrived = reinterpret_cast<int*>(ws + 256);
-  p.parts = reinterpret_cast<float*>(ws + 256 + (size_t)few_ctas(kNR) * 32);
+  p.parts = static_cast<float*>(parts);
   p.ctas = ctas - (plan != nullptr ? 1 : 0);   // all of the grid at once on the SMs
   p.plan = PromptPlan{};
   if (plan != nullptr) p.plan = prompt_plan_at(plan);
@@ -989,17 +988,20 @@ static cudaError_t launch(const moe_kv_attention_args& a, void* workspace, void*
 }
 
 template <int kD>
-static cudaError_t launch_rows(const moe_kv_attention_args& a, int nr, void* workspace, void* plan, cudaStream_t s) {
+static cudaError_t launch_rows(const moe_kv_attention_args& a, int nr, void* workspace, void* plan, void* parts,
+                               cudaStream_t s) {
   switch (nr) {
-    case 8: return launch<kD, 8>(a, workspace, plan, s);
-    case 16: return launch<kD, 16>(a, workspace, plan, s);
-    case 32: return launch<kD, 32>(a, workspace, plan, s);
-    default: return launch<kD, 64>(a, workspace, plan, s);
+    case 8: return launch<kD, 8>(a, workspace, plan, parts, s);
+    case 16: return launch<kD, 16>(a, workspace, plan, parts, s);
+    case 32: return launch<kD, 32>(a, workspace, plan, parts, s);
+    default: return launch<kD, 64>(a, workspace, plan, parts, s);
   }
 }
 
-cudaError_t launch_attn_few(const moe_kv_attention_args& a, int nr, void* workspace, void* plan, cudaStream_t s) {
-  return a.D == 128 ? launch_rows<128>(a, nr, workspace, plan, s) : launch_rows<64>(a, nr, workspace, plan, s);
+cudaError_t launch_attn_few(const moe_kv_attention_args& a, int nr, void* workspace, void* plan, void* parts,
+                            cudaStream_t s) {
+  return a.D == 128 ? launch_rows<128>(a, nr, workspace, plan, parts, s)
+                    : launch_rows<64>(a, nr, workspace, plan, parts, s);
 }
 
 }  // namespace moe

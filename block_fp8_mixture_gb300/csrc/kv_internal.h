@@ -17,11 +17,14 @@ cudaError_t launch_rope_append(const moe_rope_append_args& a, cudaStream_t s);
 // Requests with few query rows, n <= few_rows / (Hq / Hkv) tokens.  plan (nullptr: the call has no
 // longer requests) receives the blocks of the others.
 int few_rows(int G, int max_q);
-size_t few_workspace_bytes(int D, int rows);
-cudaError_t launch_attn_few(const moe_kv_attention_args& a, int rows, void* workspace, void* plan, cudaStream_t s);
-// The others, right after launch_attn_few on the same stream; `space` (256-byte aligned) is its plan.
+size_t few_counter_bytes(int rows);
+size_t few_parts_bytes(int D, int rows);
+cudaError_t launch_attn_few(const moe_kv_attention_args& a, int rows, void* workspace, void* plan, void* parts,
+                            cudaStream_t s);
+// The others, right after launch_attn_few on the same stream, whose parts are no longer needed then.
 bool prompt_fits(int T, int G, int B);
-size_t prompt_workspace_bytes(int D);
-cudaError_t launch_attn_prompt(const moe_kv_attention_args& a, int* status, void* space, cudaStream_t s);
+size_t prompt_plan_bytes();
+size_t prompt_parts_bytes(int D);
+cudaError_t launch_attn_prompt(const moe_kv_attention_args& a, int* status, void* plan, void* parts, cudaStream_t s);
 
 }  // namespace moe

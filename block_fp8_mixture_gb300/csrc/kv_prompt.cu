@@ -30,8 +30,6 @@
 // about 3300 cycles, of which the products need 2050: what is left is the chain score -> softmax -> product
 // of each tile.  Five prompts of 300 to 4000 tokens: 173 us, 1.04 PFLOP/s, the start and end of each block
 // being about 2.5 steps.
-#include <cuda_fp16.h>
-
 #include <algorithm>
 
 #include "kv_plan.cuh"
@@ -56,11 +54,11 @@ struct PromptCfg {
   static constexpr int Tiles = QBytes + KStages * KBytes + VStages * VBytes + WStages * WBytes;
   static constexpr int OutWarp = 32 * 64 * 2;            // 64 BF16 values of a warp's rows on their way out
   static constexpr int Smem = 1024 + Tiles + 8 * OutWarp + 1024 + Slots * 128 + Works * 64 + kCtaRows * 4;
-  // A part of a cut block: a row's values as FP16 after a power of two that takes the largest to 2^14 .. 2^15,
-  // with that scale, the row's maximum and its sum in FP32.  The join adds in FP32; what the 11 bits
-  // leave off is an eighth of the output's own rounding to BF16, and half the bytes are half the time.
-  static constexpr int PartWords = kCtaRows * (kD / 2 + 3);
-  static_assert(Smem <= 232448, "shared memory");
+  // A part of a cut block: a row's values as FP32 without the last 8 bits, four in three words, and the
+  // row's maximum and sum.  The join adds in FP32; what is left off, 2^-15 of a part's value, is a 128th of
+  // the output's own rounding to BF16.  (FP16 with a scale per row is a 2^-11: seen in single values where large
+  // parts cancel.)
+  static constexpr int PartWords = kCtaRows * (kD * 3 / 4 + 2);
 };
 
 // Per 16 tokens of a tile: K scale x softmax scale x log2 e, log2 V scale, 1 / V scale.
@@ -696,29 +694,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (!ok) break;
       tc_fence_after_sync();
       if (piece) {
-        float amax = 0.0f;
 #pragma unroll 1
         for (int c = 0; c < kD; c += 32) {
           uint32_t v[32];
           tmem_ld32(tO + c, v);
           tmem_ld_wait();
+          uint32_t* to = part + c * 3 / 4 * kCtaRows;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(__uint_as_float(v[i])));
+          for (int i = 0; i < 32; i += 4) {
+            // byte 3, 2 and 1 of the fourth value take the others' byte 0
+            to[(i * 3 / 4) * kCtaRows] = __byte_perm(v[i], v[i + 3], 0x3217);
+            to[(i * 3 / 4 + 1) * kCtaRows] = __byte_perm(v[i + 1], v[i + 3], 0x3216);
+            to[(i * 3 / 4 + 2) * kCtaRows] = __byte_perm(v[i + 2], v[i + 3], 0x3215);
+          }
         }
-        const int e = amax > 0.0f && amax < INFINITY ? max((int)(__float_as_uint(amax) >> 23) - 127, -100) : 14;
-        const float mul = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-#pragma unroll 1
-        for (int c = 0; c < kD; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(tO + c, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            part[(c + i) / 2 * kCtaRows] = pack_f16x2(__uint_as_float(v[i]) * mul, __uint_as_float(v[i + 1]) * mul);
-        }
-        part[kD / 2 * kCtaRows] = __float_as_uint(M);
-        part[(kD / 2 + 1) * kCtaRows] = __float_as_uint(l);
-        part[(kD / 2 + 2) * kCtaRows] = (uint32_t)(127 - 14 + e) << 23;
+        part[kD * 3 / 4 * kCtaRows] = __float_as_uint(M);
+        part[(kD * 3 / 4 + 1) * kCtaRows] = __float_as_uint(l);
       } else {
         // 64 values at a time through shared memory, so that the stores cover whole lines of a row
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
@@ -828,7 +819,7 @@ __global__ void __launch_bounds__(kCtaRows) k_prompt_join(const PromptParams p) 
   auto part = [&](int i) { return p.parts + (size_t)places[i] * C::PartWords + threadIdx.x; };
   float M = -INFINITY;
 #pragma unroll 8
-  for (int i = 0; i < count; ++i) M = fmaxf(M, __uint_as_float(part(i)[kD / 2 * kCtaRows]));
+  for (int i = 0; i < count; ++i) M = fmaxf(M, __uint_as_float(part(i)[kD * 3 / 4 * kCtaRows]));
   float l = 0.0f, acc[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
@@ -836,19 +827,20 @@ __global__ void __launch_bounds__(kCtaRows) k_prompt_join(const PromptParams p) 
 #pragma unroll 2
   for (int i = 0; i < count; ++i) {
     const uint32_t* o = part(i);
-    const float m = __uint_as_float(o[kD / 2 * kCtaRows]), lp = __uint_as_float(o[(kD / 2 + 1) * kCtaRows]);
-    const float scale = __uint_as_float(o[(kD / 2 + 2) * kCtaRows]);
-    uint32_t x[8];
+    const float m = __uint_as_float(o[kD * 3 / 4 * kCtaRows]), lp = __uint_as_float(o[(kD * 3 / 4 + 1) * kCtaRows]);
+    uint32_t x[12];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = o[(c0 / 2 + j) * kCtaRows];
+    for (int j = 0; j < 12; ++j) x[j] = o[(c0 * 3 / 4 + j) * kCtaRows];
     if (m == -INFINITY) continue;    // a part whose tokens this row does not see has an empty sum
-    const float wgt = m == M ? 1.0f : exp2_approx(m - M), f = wgt * scale;
+    const float wgt = m == M ? 1.0f : exp2_approx(m - M);
     l = __fmaf_rn(lp, wgt, l);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-      acc[2 * j] = __fmaf_rn(v.x, f, acc[2 * j]);
-      acc[2 * j + 1] = __fmaf_rn(v.y, f, acc[2 * j + 1]);
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t* y = x + 3 * j;
+      const uint32_t last = ((y[0] & 0xFF) << 24) | ((y[1] & 0xFF) << 16) | ((y[2] & 0xFF) << 8);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) acc[4 * j + k] = __fmaf_rn(__uint_as_float(y[k] & ~0xFFu), wgt, acc[4 * j + k]);
+      acc[4 * j + 3] = __fmaf_rn(__uint_as_float(last), wgt, acc[4 * j + 3]);
     }
   }
   const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
@@ -871,10 +863,12 @@ bool prompt_fits(int T, int G, int B) {
   return (long long)T * G / kBlockRows + B <= kMaxBlocks;
 }
 
-size_t prompt_workspace_bytes(int D) { return kPlanBytes + (size_t)2 * kPromptCtas * kCtaRows * (D / 2 + 3) * 4; }
+size_t prompt_plan_bytes() { return kPlanBytes; }
+
+size_t prompt_parts_bytes(int D) { return (size_t)2 * kPromptCtas * kCtaRows * (D * 3 / 4 + 2) * 4; }
 
 template <int kD>
-static cudaError_t launch_prompt(const moe_kv_attention_args& a, int* status, void* space,
+static cudaError_t launch_prompt(const moe_kv_attention_args& a, int* status, void* plan, void* parts,
                                  cudaStream_t s) {
   using C = PromptCfg<kD>;
   CUtensorMap tmK, tmV;
@@ -890,8 +884,8 @@ static cudaError_t launch_prompt(const moe_kv_attention_args& a, int* status, vo
   p.G = a.Hq / a.Hkv;
   p.page_shift = __builtin_ctz((unsigned)a.page_size);
   p.magic = p.G == 1 ? 0 : (uint32_t)(((1ull << 32) + p.G - 1) / p.G);
-  p.plan = prompt_plan_at(space);
-  p.parts = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(space) + kPlanBytes);
+  p.plan = prompt_plan_at(plan);
+  p.parts = static_cast<uint32_t*>(parts);
   p.status = status;
   const int pairs = p.plan.pairs;
   // nothing is cut where no block can see enough tiles: one launch less (3 x 104 tokens: 15.6 -> 13.8 us)
@@ -917,8 +911,9 @@ static cudaError_t launch_prompt(const moe_kv_attention_args& a, int* status, vo
   return launch_pdl(k_prompt_join<kD>, dim3(pairs, kD / 16, 2), dim3(kCtaRows), 0, s, p);
 }
 
-cudaError_t launch_attn_prompt(const moe_kv_attention_args& a, int* status, void* space, cudaStream_t s) {
-  return a.D == 128 ? launch_prompt<128>(a, status, space, s) : launch_prompt<64>(a, status, space, s);
+cudaError_t launch_attn_prompt(const moe_kv_attention_args& a, int* status, void* plan, void* parts,
+                               cudaStream_t s) {
+  return a.D == 128 ? launch_prompt<128>(a, status, plan, parts, s) : launch_prompt<64>(a, status, plan, parts, s);
 }
 
 }  // namespace moe

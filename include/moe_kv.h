@@ -138,8 +138,8 @@ moe_status moe_rope_append(const moe_rope_append_args* args, moe_stream_t stream
  * codes outside every row's view (stale rows of the last page, other pages) never matter.
  * Supported: 1 <= num_pages, Hq % Hkv == 0, Hq / Hkv <= 64, sm_scale finite and > 0, 1 <= B <= 4096, max_q >= 1.
  * Strides in elements, multiples of 8.
- * Parts of a long request are kept in the workspace on the way: FP32 with few query rows, FP16 with a
- * scale per row (and FP32 statistics) with many, which is less than the rounding of out.
+ * Parts of a long request are kept in the workspace on the way: FP32 with few query rows, FP32
+ * without the last 8 bits (with whole FP32 statistics) with many: 2^-15, where the rounding of out is 2^-8.
  * MOE_ERR_INVALID_ARG with num_pages 0; MOE_ERR_UNSUPPORTED_SHAPE where the work would pass 32-bit counts:
  * T * (Hq / Hkv) / 512 + B > 65536 with more rows than 64 in a request, or
  * Hkv * (B * max_pages * page_size / 128 + 4 * B) >= 2^31 - 2^20.
