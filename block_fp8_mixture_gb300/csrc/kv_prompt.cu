@@ -24,11 +24,11 @@
 // Work: rounds over the blocks, longest first, and a last one whose tiles are poured over the pairs up to
 // a common level (kv_plan.cuh).  Blocks that this cuts along the cache k_prompt_join adds up, in order.
 //
-// 4096 tokens after 28000, 32 / 8 heads of 128: 1.28 ms, 1.58 PFLOP/s, 84% of the measured 16-bit rate.  At
+// 4096 tokens after 28000, 32 / 8 heads of 128: 1.30 ms, 1.55 PFLOP/s, 82% of the measured 16-bit rate.  At
 // 1.42 ms the other layouts took: one CTA per block of 256 rows 1.59 ms; V read past shared memory 1.72 ms;
 // two threads a row 1.52 ms; an issuing warp per tile of rows 1.85 ms.  A step of 512 rows x 128 tokens takes
 // about 3300 cycles, of which the products need 2050: what is left is the chain score -> softmax -> product
-// of each tile.  Five prompts of 300 to 4000 tokens: 173 us, 1.04 PFLOP/s, the start and end of each block
+// of each tile.  Five prompts of 300 to 4000 tokens: 175 us, 1.03 PFLOP/s, the start and end of each block
 // being about 2.5 steps.
 #include <algorithm>
 
@@ -263,8 +263,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (warp < 4) {
     // One idle warp triggers the join's launch, which waits for this kernel's end all the same (in every warp
     // this costs 2% of a chunk).  Where no join follows, the caller's next kernel would only be in the way.
-    if (warp == 3 && p.join) grid_dep_launch_dependents();
     regs_down<kRegsIssue>();
+    if (warp == 3 && p.join) grid_dep_launch_dependents();
     if (warp == 0) {
       // -------------------------------------------------------------------- producer
       const int npg = kTile >> p.page_shift, P = 1 << p.page_shift;
@@ -695,13 +695,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       tc_fence_after_sync();
       if (piece) {
 #pragma unroll 1
-        for (int c = 0; c < kD; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(tO + c, v);
+        for (int c = 0; c < kD; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(tO + c, v);
           tmem_ld_wait();
           uint32_t* to = part + c * 3 / 4 * kCtaRows;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
+          for (int i = 0; i < 16; i += 4) {
             // byte 3, 2 and 1 of the fourth value take the others' byte 0
             to[(i * 3 / 4) * kCtaRows] = __byte_perm(v[i], v[i + 3], 0x3217);
             to[(i * 3 / 4 + 1) * kCtaRows] = __byte_perm(v[i + 1], v[i + 3], 0x3216);
