@@ -28,7 +28,7 @@ struct AttentionSpace {
 };
 static AttentionSpace attention_space(int D, int rows, bool prompts) {
   AttentionSpace w;
-  w.plan = few_counter_bytes(rows);
+  w.plan = few_counter_bytes();
   w.parts = w.plan + (prompts ? prompt_plan_bytes() : 0);
   w.total = w.parts + std::max(few_parts_bytes(D, rows), prompts ? prompt_parts_bytes(D) : (size_t)0);
   return w;

@@ -27,8 +27,8 @@
 //
 // 128 requests of 8k to 16k tokens, 64 / 8 heads of 128: 447 us, 6.85 TB/s, at the measured copy rate (6.77).
 // 32 / 8 heads, one request of 128k: 53 us, 5.1 TB/s; of 4k: 11 us, of which start and join are 9.  61 of 6
-// to 8190 tokens, 40 / 8 heads: 38 us, 4.0 TB/s.  Heads of 64: 5.1 TB/s at best, a tile's chain of scores, softmax and product
-// takes longer than its bytes (three CTAs an SM instead of two: registers spill, 102 -> 108 us).
+// to 8190 tokens, 40 / 8 heads: 38 us, 4.0 TB/s.  Heads of 64: 5.1 TB/s at best, a tile's chain of scores,
+// softmax and product takes longer than its bytes (three CTAs an SM instead of two: registers spill, 102 -> 108 us).
 #include <algorithm>
 
 #include "kv_plan.cuh"
@@ -956,7 +956,9 @@ int few_rows(int G, int max_q) {
 
 static int few_ctas(int nr) { return nr <= 16 ? 304 : 152; }   // at most; 152 SMs
 
-size_t few_counter_bytes(int nr) { return (256 + (size_t)few_ctas(nr) * 32 + 255) & ~(size_t)255; }
+// The same for all variants: calls with other row counts may use the workspace in between, and must leave
+// the counters at zero.
+size_t few_counter_bytes() { return (256 + (size_t)few_ctas(8) * 32 + 255) & ~(size_t)255; }
 
 size_t few_parts_bytes(int D, int nr) { return (size_t)2 * few_ctas(nr) * nr * (D + 2) * 4; }
 

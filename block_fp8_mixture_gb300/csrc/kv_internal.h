@@ -17,7 +17,7 @@ cudaError_t launch_rope_append(const moe_rope_append_args& a, cudaStream_t s);
 // Requests with few query rows, n <= few_rows / (Hq / Hkv) tokens.  plan (nullptr: the call has no
 // longer requests) receives the blocks of the others.
 int few_rows(int G, int max_q);
-size_t few_counter_bytes(int rows);
+size_t few_counter_bytes();
 size_t few_parts_bytes(int D, int rows);
 cudaError_t launch_attn_few(const moe_kv_attention_args& a, int rows, void* workspace, void* plan, void* parts,
                             cudaStream_t s);

@@ -802,7 +802,8 @@ __global__ void __launch_bounds__(kCtaRows) k_prompt_join(const PromptParams p) 
 #pragma unroll
     for (int i = 0; i < (kPromptPairs + 31) / 32; ++i) {
       const int c = 32 * i + threadIdx.x;
-      const bool here = c < p.plan.pairs && prompt_cut(tail.bound[c] - at, e.z) < prompt_cut(tail.bound[c + 1] - at, e.z);
+      const bool here =
+          c < p.plan.pairs && prompt_cut(tail.bound[c] - at, e.z) < prompt_cut(tail.bound[c + 1] - at, e.z);
       const uint32_t mask = __ballot_sync(~0u, here);
       const int k = n + __popc(mask & ((1u << threadIdx.x) - 1));
       if (here) places[k] = 2 * (2 * c + (k == 0 ? 1 : 0)) + blockIdx.z;

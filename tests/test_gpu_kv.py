@@ -466,6 +466,23 @@ def test_attention_prompts_shared_by_pairs(D, P, Hq, Hkv, ctx, add, window):
     assert torch.equal(again[:n], first[:n])
 
 
+def test_attention_one_workspace_for_all_row_counts():
+    """A workspace for the largest max_q serves calls with any smaller one, in any order: what one variant
+    leaves behind must not be another's counters."""
+    rng = np.random.default_rng(31)
+    Hq, Hkv, D, P = 8, 1, 64, 32
+    ws = moe.alloc_kv_attention_workspace(Hq, Hkv, D, 300)
+    cases = {n: attention_case(rng, [9000, 700], [n, 1], P, Hq, Hkv, D, poison=False) for n in (1, 2, 4, 8, 300)}
+    first = {}
+    for n in (1, 8, 1, 4, 1, 2, 300, 1, 300, 8, 2, 4, 1):
+        if n not in first:
+            first[n] = check_attention(*cases[n], max_q=n, ws=ws, what=n).clone()
+        else:
+            q, _, cache, _, _, t = cases[n]
+            got = moe.kv_attention(q, cache, t.block_table, t.kv_len, t.tok_start, ws, max_q=n)
+            assert torch.equal(got, first[n]), n
+
+
 # ------------------------------------------------------------------------------- the pieces together
 def test_paged_attention_over_steps():
     """PagedAttention over steps that add, finish, refill and roll back requests, on two layers: every
