@@ -11,7 +11,11 @@
 // accumulation in fp32 and costs no second read of A: a row of Q, scaled by a power of two, into
 // two terms (the second x 32: 8 bits, absolute error 2^-15 of the largest value), a row of P into
 // three (x 1, x 32, x 1024: 12 bits down to 2^-13 of the running maximum, 8 at 2^-17, 4 at 2^-21).
-// The page's K scale multiplies the score, its V scale the probability, relative to the tile's largest.
+// The page's K scale multiplies the score.  Its V scale goes into the exponent: with f = K scale x softmax
+// scale and lv = log2 V scale, p' = 2^(s f + lv - M), where M is the row's running maximum of s f + lv.  Then
+// O = sum p' code needs no scale, the row sum is sum p' / V scale, and the terms keep their bits however far
+// apart the scales of a tile's pages are.  (p' relative to the tile's largest V scale loses a bit of P for every
+// bit of the ratio past 2^14, and a row whose weight lies on the page with the small scale its result.)
 //
 // The work is dealt out evenly, whatever the lengths: an item (request, head) weighs kItemUnits, what
 // its start and end cost, and one unit per 128-token tile; CTA c takes the tiles that lie in the c-th of
@@ -22,7 +26,7 @@
 //   warp 0      producer: lane i fetches page i of the tile (TMA), its scales and the tile's bounds
 //   warp 1      MMA issuer
 //   warps 2..   one warpgroup per 8 or 16 rows: thread = token for the scores, = d for the output
-// The maximum that scores are taken relative to moves only when a score passes it by 8 x (2^3): then
+// The maximum that scores are taken relative to moves only when one passes it by 8 x (2^3): then
 // all threads of the warpgroup reduce the tile's maximum and rescale, else a vote is all it costs.
 //
 // 128 requests of 8k to 16k tokens, 64 / 8 heads of 128: 447 us, 6.85 TB/s, at the measured copy rate (6.77).
@@ -35,8 +39,8 @@
 
 namespace moe {
 
-constexpr float kPScale = 32.0f;           // P = 1 at the running maximum becomes 32 (up to 256)
-constexpr float kGrow = 3.0f;              // log2 by which a score may pass the maximum
+constexpr float kPBias = 5.0f;             // log2 of p' at the running maximum
+constexpr float kGrow = 3.0f;              // log2 by which a score may pass the maximum: p' stays below 256
 constexpr int kBatch = 8;                  // tiles whose pages are looked up together, at most
 constexpr int kItemUnits = 3;              // start and end of an item, in tiles
 constexpr int kJoinGroup = 16;             // CTAs whose parts are added first where an item has many parts
@@ -61,7 +65,7 @@ struct FewCfg {
   static constexpr int OCol = 2 * SCols;
   static constexpr int TmemCols = kNR == 8 ? 64 : kNR == 16 ? 128 : kNR == 32 ? 256 : 512;
   static constexpr int LdCols = kNR == 64 || kNR == 8 ? 8 : 16;   // 64 rows: 96 registers a thread
-  static constexpr int SlotBytes = 128;
+  static constexpr int SlotBytes = 160;
   static constexpr int CtrlBytes = 1024 + Stages * SlotBytes + WGs * 5 * 16 * 4;
   static constexpr int Smem = 1024 + Stages * StageBytes + QBytes + PBytes + CtrlBytes;
   static_assert(OCol + 16 * PPieces <= TmemCols, "tensor memory");
@@ -71,8 +75,8 @@ struct FewCfg {
 // What the softmax warps need of a tile.
 struct FewSlot {
   float kf[kMaxTilePages];     // K scale x sm_scale x log2 e
-  float vr[kMaxTilePages];     // V scale / vref x kPScale
-  float vref;
+  float lv[kMaxTilePages];     // log2 V scale
+  float iv[kMaxTilePages];     // 1 / V scale
   int token0;                  // first token of the tile
   int lo, hi;                  // tokens that some row sees
   int pos0, rows, q0, head;    // position of query token 0, live rows, row of it in q, key/value head
@@ -80,9 +84,9 @@ struct FewSlot {
   int part;                    // workspace part that the segment fills, -1: the whole item is here
   int first_cta, parts;        // CTAs that share the item
   int first_part;              // part of the first of them; the others' first segment has part 2 x CTA
-  int pad[3];
+  int pad[4];
 };
-static_assert(sizeof(FewSlot) == 128, "slot");
+static_assert(sizeof(FewSlot) == 160, "slot");
 
 struct FewParams {
   moe_kv_attention_args a;
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         const bool live = now.page >= 0 && now.page < p.a.num_pages;
         const uint32_t pages = __ballot_sync(~0u, live);
         const uint32_t bytes = __popc((pages >> (group * npg)) & ((1u << npg) - 1)) * P * kD;
-        float kf = 0.0f, vr = 0.0f, vref = 0.0f;
+        float kf = 0.0f, lv = 0.0f, iv = 0.0f;
         for (int k = 0; k < batch; ++k) {
           if (!__any_sync(~0u, group == k && now.live)) break;
           const int s = it % C::Stages;
@@ -493,21 +497,17 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           }
           if (k == 0) {
             // the scales are needed only now that the batch's first copies are on their way
-            vref = live ? vs : 0.0f;
-#pragma unroll
-            for (int d = kMaxTilePages / 2; d; d >>= 1) {
-              const float other = __shfl_xor_sync(~0u, vref, d);
-              if (d < npg) vref = fmaxf(vref, other);
-            }
             kf = ks * p.a.sm_scale * kLog2e;
-            vr = vref > 0.0f ? __fdiv_rn(vs, vref) * kPScale : (vs == vs ? 0.0f : vs);
+            const float v = vs >= 0.0f ? fmaxf(vs, 1e-30f) : vs;
+            lv = log2f(v);
+            iv = __fdiv_rn(1.0f, v);
           }
           if (mine) {
             slot.kf[pi] = kf;
-            slot.vr[pi] = vr;
+            slot.lv[pi] = lv;
+            slot.iv[pi] = iv;
             if (leader) {
               const bool end = now.tile == now.item.tiles - 1, last = now.live == 2;
-              slot.vref = vref;
               slot.token0 = (now.item.tile0 + now.tile) * kTile;
               slot.lo = now.item.lo;
               slot.hi = now.item.hi;
@@ -602,7 +602,6 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
       constexpr int kRowLanes = 32 / kR;                // lanes that share a row's reduction
       float m[kR];
       f32x2 l[kR / 2], acc[kR / 2];                     // two rows each
-      float vref_prev = 0.0f;
       // A wait that runs out only marks the thread: the warpgroup leaves together, at the next vote,
       // so no barrier is left waiting.
       bool pending = false, bad = false, begin = true;
@@ -612,8 +611,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           return;
         }
         tc_fence_after_sync();
-        const float f = vref_prev * (1.0f / kPScale);
-        const f32x2 f2 = pack2(f, f), step = pack2(1.0f / kTermStep, 1.0f / kTermStep);
+        const f32x2 step = pack2(1.0f / kTermStep, 1.0f / kTermStep);
 #pragma unroll
         for (int r0s = 0; r0s < kR; r0s += C::LdCols) {
           uint32_t t[3][C::LdCols];
@@ -627,7 +625,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
 #pragma unroll
           for (int r = 0; r < C::LdCols / 2; ++r)
             acc[r0s / 2 + r] =
-                fma2(fma2(fma2(pair(2, r), step, pair(1, r)), step, pair(0, r)), f2, acc[r0s / 2 + r]);
+                add2(fma2(fma2(pair(2, r), step, pair(1, r)), step, pair(0, r)), acc[r0s / 2 + r]);
         }
         tc_fence_before_sync();
       };
@@ -706,7 +704,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         }
         // scores of this thread's token
         const int page = tl >> p.page_shift;
-        const float kf = slot.kf[page], vr = slot.vr[page];
+        const float kf = slot.kf[page], lv = slot.lv[page], iv = slot.iv[page];
         const int j = slot.token0 + tl;
         const bool edge = slot.token0 < slot.lo || slot.token0 + kTile > slot.hi;
         // rows [from, to) of the warpgroup see the token; rows past the live ones may see anything
@@ -721,7 +719,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         tc_fence_after_sync();
         float sc[kR];
         {
-          const f32x2 step = pack2(1.0f / kTermStep, 1.0f / kTermStep), kf2 = pack2(kf, kf);
+          const f32x2 step = pack2(1.0f / kTermStep, 1.0f / kTermStep), kf2 = pack2(kf, kf), lv2 = pack2(lv, lv);
 #pragma unroll
           for (int r0s = 0; r0s < kR; r0s += C::LdCols) {
             uint32_t t[C::LdCols], t2[C::LdCols];
@@ -738,7 +736,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
                 const f32x2 v = fma2(pack2(__uint_as_float(t2[x]), __uint_as_float(t2[x + 1])), step,
                                      pack2(__uint_as_float(t[x]), __uint_as_float(t[x + 1])));
                 const f32x2 f = mul2(i ? pack2(qs.z, qs.w) : pack2(qs.x, qs.y), kf2);
-                unpack2(mul2(v, f), sc[r0s + x], sc[r0s + x + 1]);
+                unpack2(fma2(v, f, lv2), sc[r0s + x], sc[r0s + x + 1]);
               }
             }
           }
@@ -751,7 +749,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         }
         bool grow = false;
 #pragma unroll
-        for (int r = 0; r < kR; ++r) grow |= sc[r] > m[r] + kGrow;
+        for (int r = 0; r < kR; ++r) grow |= sc[r] > m[r] + (kGrow + kPBias);
         if (vote_any<128>(1 + wg, grow || bad)) {
           if (vote_any<128>(1 + wg, bad)) break;
           // the maximum of some row moved: bring what is outstanding in, then rescale
@@ -769,7 +767,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
 #pragma unroll
             for (int i = r; i < r + 2; ++i) {
               const float t = fmaxf(fmaxf(wred[i], wred[16 + i]), fmaxf(wred[32 + i], wred[48 + i]));
-              const float mn = fmaxf(m[i], t);
+              const float mn = fmaxf(m[i], t - kPBias);
               alpha[i - r] = m[i] == mn ? 1.0f : exp2_approx(m[i] - mn);
               m[i] = mn;
             }
@@ -785,8 +783,8 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           float p0, p1;
           unpack2(add2(pack2(sc[r], sc[r + 1]), pack2(-m[r], -m[r + 1])), p0, p1);
           const f32x2 pr = pack2(exp2_approx(p0), exp2_approx(p1));
-          l[r / 2] = add2(l[r / 2], pr);
-          unpack2(mul2(pr, pack2(vr, vr)), p0, p1);
+          l[r / 2] = fma2(pr, pack2(iv, iv), l[r / 2]);
+          unpack2(pr, p0, p1);
           uint32_t h2 = pack_f16x2(p0, p1);
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
@@ -814,7 +812,6 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
             for (int i = 0; i < kD / 16; ++i) row[i] = make_uint4(0, 0, 0, 0);
           }
         }
-        vref_prev = slot.vref;
         pending = true;
         const int part = slot.part, first_cta = slot.first_cta, parts = slot.parts, first_part = slot.first_part;
         const int flags = slot.flags;

@@ -1,0 +1,50 @@
+"""GPU: the paged 8-bit cache where its ranges end, against the CPU statement (oracle/kv_ref.py).  The bounds
+are those of test_gpu_kv.py."""
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+import block_fp8_mixture_gb300 as moe  # noqa: E402
+from oracle import kv_ref  # noqa: E402
+from test_gpu_kv import attention_case, check_attention, dev, host  # noqa: E402
+
+
+@pytest.fixture(autouse=True)
+def _library():
+    moe.load_library(build_if_missing=True)
+
+
+def device_cache(codes, scale):
+    return moe.KVCache(*(dev(a) for a in (codes[0], codes[1], scale[0], scale[1])))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("P,Hq,Hkv,add", [
+    (16, 4, 2, 1), (32, 8, 1, 1), (64, 16, 1, 1), (16, 24, 1, 1), (32, 8, 2, 8), (16, 64, 1, 1), (32, 4, 2, 150),
+])
+@pytest.mark.parametrize("ratio", [-12, -20, -30, 25])
+def test_attention_weight_on_a_page_with_another_v_scale(ratio, P, Hq, Hkv, add, D):
+    """Even heads put all their weight on one page, odd ones on all others, and that page's V scale is
+    2^ratio of the others'.  The scores of the two kinds of pages are 64 (D = 128: 90) apart in natural
+    units: exp(-64) = 2^-92, so what is not meant adds nothing even at ratio -30."""
+    rng = np.random.default_rng(P + Hq + D)
+    L = 330
+    q, xq, _, codes, scale, t = attention_case(rng, [L], [add], P, Hq, Hkv, D)
+    table = host(t)["block_table"][0]
+    page = table[kv_ref.pages(L, P) // 2]
+    codes[0][page] = 0x38                                 # keys of the page: ones
+    scale[0][page] = 1.0
+    others = [x for x in table[:kv_ref.pages(L + add, P)] if x != page]
+    scale[0][others] = 2.0 ** -20
+    scale[1][others] = 2.0 ** -7
+    scale[1][page] = 2.0 ** (ratio - 7)
+    xq = np.full(xq.shape, 8.0, np.float32)
+    xq[:, 1::2] = -8.0
+    q = torch.from_numpy(xq).to(torch.bfloat16).cuda()
+    check_attention(q, xq, device_cache(codes, scale), codes, scale, t, add)
