@@ -99,22 +99,23 @@ struct FewParams {
   PromptPlan plan;
 };
 
-// Lengths of request b: cached tokens, query tokens, whether this kernel handles it, and the tiles
-// that hold the tokens its rows see (one, empty, when they see nothing).
+// Request b: position of its first query token, query tokens (of more than max_q the first ones), and the
+// tiles that hold the tokens its rows see (one, empty, when they see nothing; none: not this kernel's).
 struct FewItem {
-  int L, n, q0, lo, hi, tile0, tiles;
+  int pos0, n, q0, lo, hi, tile0, tiles;
 };
 
 template <int kNR>
 __device__ __forceinline__ FewItem few_item(const FewParams& p, int b) {
   FewItem it;
   it.q0 = p.a.tok_start[b];
-  it.n = p.a.tok_start[b + 1] - it.q0;
-  it.L = min(max(p.a.kv_len[b], 0), p.a.max_pages << p.page_shift);
+  const int n = p.a.tok_start[b + 1] - it.q0;
+  it.n = min(n, p.a.max_q);
+  it.pos0 = min(max(p.a.kv_len[b], 0), p.a.max_pages << p.page_shift) - n;
   it.lo = it.hi = it.tile0 = it.tiles = 0;
-  if (it.n >= 1 && it.n <= kNR / p.G && it.q0 >= 0 && it.q0 + it.n <= p.a.T) {
-    it.hi = it.L;
-    if (p.a.window > 0) it.lo = max(0, it.L - it.n - p.a.window + 1);
+  if (n >= 1 && it.n <= kNR / p.G && it.q0 >= 0 && it.q0 + n <= p.a.T) {
+    it.hi = max(0, it.pos0 + it.n);
+    if (p.a.window > 0) it.lo = max(0, it.pos0 - p.a.window + 1);
     it.tile0 = it.lo / kTile;
     it.tiles = max(1, (it.hi + kTile - 1) / kTile - it.tile0);
   }
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
               slot.token0 = (now.item.tile0 + now.tile) * kTile;
               slot.lo = now.item.lo;
               slot.hi = now.item.hi;
-              slot.pos0 = now.item.L - now.item.n;
+              slot.pos0 = now.item.pos0;
               slot.rows = now.item.n * p.G;
               slot.q0 = now.item.q0;
               slot.head = now.h;

@@ -48,3 +48,36 @@ def test_attention_weight_on_a_page_with_another_v_scale(ratio, P, Hq, Hkv, add,
     xq[:, 1::2] = -8.0
     q = torch.from_numpy(xq).to(torch.bfloat16).cuda()
     check_attention(q, xq, device_cache(codes, scale), codes, scale, t, add)
+
+
+@pytest.mark.parametrize("Hq,Hkv,max_q,n", [
+    (8, 1, 1, [3, 1, 2]),                 # 8 rows: three tokens would not fit
+    (8, 2, 2, [5, 1, 3]),
+    (4, 4, 3, [4, 0, 9]),                 # 8 rows hold four tokens too
+    (8, 1, 8, [20, 8, 9]),                # 64 rows
+    (4, 2, 70, [150, 3, 71]),             # prompts with a short request among them
+])
+@pytest.mark.parametrize("window", [0, 40])
+def test_attention_cuts_requests_to_max_q(Hq, Hkv, max_q, n, window):
+    """The first max_q rows of a longer request are those of the whole request, the later ones are left as
+    they were, and cached tokens that only those would see may hold anything."""
+    rng = np.random.default_rng(Hq + max_q)
+    D, P = 64, 16
+    q, xq, _, codes, scale, t = attention_case(rng, [200, 30, 0], n, P, Hq, Hkv, D, extra_tokens=2)
+    h = host(t)
+    ref, mag = kv_ref.attention(xq, codes, scale, h["block_table"], h["kv_len"], h["tok_start"], D ** -0.5, window)
+    keep = np.zeros(q.shape[0], bool)
+    codes = codes.copy()
+    for b, (m, L) in enumerate(zip(n, h["kv_len"])):
+        a = h["tok_start"][b]
+        keep[a:a + min(m, max_q)] = True
+        for j in range(L - m + min(m, max_q), L):
+            codes[:, h["block_table"][b, j // P], :, j % P] = 0x7F
+    out = torch.full((q.shape[0], Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = moe.alloc_kv_attention_workspace(Hq, Hkv, D, max_q)
+    moe.kv_attention(q, device_cache(codes, scale), t.block_table, t.kv_len, t.tok_start, ws, max_q=max_q,
+                     window=window, out=out)
+    assert moe.last_device_status(ws) == moe.MOE_OK
+    got = out.float().cpu().numpy().astype(np.float64)
+    assert (got[~keep] == 7.0).all()
+    assert (np.abs(got - ref)[keep] <= (2.0 ** -8 * np.abs(ref) + 2.0 ** -9 * mag)[keep]).all()
