@@ -328,7 +328,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (lane < 8) {
             slots[si].kf[lane] = gk * p.a.sm_scale * kLog2e;
             const float v = gv >= 0.0f ? fmaxf(gv, 1e-30f) : gv;
-            slots[si].lv[lane] = log2f(v);
+            // a K scale that is NaN goes in here: the lower bound on f would hide it
+            slots[si].lv[lane] = gk == gk ? log2f(v) : gk;
             slots[si].iv[lane] = 1.0f / v;
           }
           __syncwarp();

@@ -134,8 +134,9 @@ moe_status moe_rope_append(const moe_rope_append_args* args, moe_stream_t stream
  * Scores, softmax statistics and sums are fp32; out is rounded once to BF16.
  * max_q is an upper bound of the n (requests with more tokens are cut to max_q tokens by the caller's
  * mistake: their later rows are left unwritten).
- * A NaN code among the tokens that some row of the call sees may reach other rows of the same request;
- * codes outside every row's view (stale rows of the last page, other pages) never matter.
+ * A NaN among the codes and scales of the tokens that a row sees makes the row NaN (a V code: that value of
+ * it) and may reach other rows of the same request; codes outside every row's view (stale rows of the last
+ * page, other pages) never matter.
  * Supported: 1 <= num_pages, Hq % Hkv == 0, Hq / Hkv <= 64, sm_scale finite and > 0, 1 <= B <= 4096, max_q >= 1.
  * Strides in elements, multiples of 8.
  * Parts of a long request are kept in the workspace on the way: FP32 with few query rows, FP32

@@ -81,3 +81,22 @@ def test_attention_cuts_requests_to_max_q(Hq, Hkv, max_q, n, window):
     got = out.float().cpu().numpy().astype(np.float64)
     assert (got[~keep] == 7.0).all()
     assert (np.abs(got - ref)[keep] <= (2.0 ** -8 * np.abs(ref) + 2.0 ** -9 * mag)[keep]).all()
+
+
+@pytest.mark.parametrize("add", [1, 4, 130])
+@pytest.mark.parametrize("which", [0, 1])
+def test_attention_nan_scale_is_seen(which, add):
+    """A page whose K or V scale is NaN: every row that sees a token of it is NaN, other requests are not."""
+    rng = np.random.default_rng(add)
+    P, Hq, Hkv, D = 32, 4, 2, 64
+    q, xq, _, codes, scale, t = attention_case(rng, [300, 90], [add, add], P, Hq, Hkv, D)
+    h = host(t)
+    want = kv_ref.attention(xq, codes, scale, h["block_table"], h["kv_len"], h["tok_start"], D ** -0.5)
+    scale = scale.copy()
+    scale[which, h["block_table"][0, 3], 1] = np.nan          # head 1 of the first request
+    ws = moe.alloc_kv_attention_workspace(Hq, Hkv, D, add)
+    got = moe.kv_attention(q, device_cache(codes, scale), t.block_table, t.kv_len, t.tok_start, ws, max_q=add)
+    g = got.float().cpu().numpy().astype(np.float64)
+    assert np.isnan(g[:add, 2:]).all()
+    ok = np.abs(g - want[0]) <= 2.0 ** -8 * np.abs(want[0]) + 2.0 ** -9 * want[1]
+    assert ok[add:].all() and ok[:add, :2].all()
