@@ -833,7 +833,8 @@ __global__ void __launch_bounds__(kCtaRows) k_prompt_join(const PromptParams p) 
     uint32_t x[12];
 #pragma unroll
     for (int j = 0; j < 12; ++j) x[j] = o[(c0 * 3 / 4 + j) * kCtaRows];
-    if (m == -INFINITY) continue;    // a part whose tokens this row does not see has an empty sum
+    // a part whose tokens this row does not see has an empty sum; one that holds nothing but NaN has no maximum either
+    if (m == -INFINITY && lp == lp) continue;
     const float wgt = m == M ? 1.0f : exp2_approx(m - M);
     l = __fmaf_rn(lp, wgt, l);
 #pragma unroll

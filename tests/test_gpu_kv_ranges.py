@@ -100,3 +100,18 @@ def test_attention_nan_scale_is_seen(which, add):
     assert np.isnan(g[:add, 2:]).all()
     ok = np.abs(g - want[0]) <= 2.0 ** -8 * np.abs(want[0]) + 2.0 ** -9 * want[1]
     assert ok[add:].all() and ok[:add, :2].all()
+
+
+@pytest.mark.parametrize("pages", [(8, 15), (0, 29)])
+@pytest.mark.parametrize("which", [0, 1])
+def test_attention_nan_scales_in_parts_of_cut_blocks(which, pages):
+    """Some or all of the tiles that a cut block sees have NaN scales.  A part of it that holds nothing else has
+    no maximum; it must not be taken for one whose tokens the row does not see."""
+    rng = np.random.default_rng(5)
+    P, Hq, Hkv, D, add = 128, 8, 2, 128, 700
+    q, _, _, codes, scale, t = attention_case(rng, [3000], [add], P, Hq, Hkv, D)
+    scale = scale.copy()
+    scale[which, host(t)["block_table"][0, slice(*pages)], 0] = np.nan
+    ws = moe.alloc_kv_attention_workspace(Hq, Hkv, D, add)
+    got = moe.kv_attention(q, device_cache(codes, scale), t.block_table, t.kv_len, t.tok_start, ws, max_q=add)
+    assert torch.isnan(got[:, :4].float()).all() and torch.isfinite(got[:, 4:].float()).all()
