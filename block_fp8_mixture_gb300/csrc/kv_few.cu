@@ -662,7 +662,8 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
           // amax x mul in [128, 256)
           const int e = amax > 0.0f ? max((int)(__float_as_uint(amax) >> 23) - 127, -100) : 0;
-          const float mul = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+          // (0 where a value is infinite: its code becomes NaN, where a saturated one would make a finite score)
+          const float mul = e == 128 ? 0.0f : __uint_as_float((uint32_t)(127 + 7 - e) << 23);
           uint32_t t1[kV / 4], t2[kV / 4];
 #pragma unroll
           for (int i = 0; i < kV / 4; ++i) {

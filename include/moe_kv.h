@@ -132,6 +132,7 @@ moe_status moe_rope_append(const moe_rope_append_args* args, moe_stream_t stream
  * h / (Hq / Hkv).  A row that sees nothing (kv_len[b] < n, or kv_len[b] = 0) is zero.  Rows of q past
  * tok_start[B] are neither read nor written.
  * Scores, softmax statistics and sums are fp32; out is rounded once to BF16.
+ * A row that sees something and whose q holds an infinity or a NaN is NaN.
  * max_q is an upper bound of the n (requests with more tokens are cut to max_q tokens by the caller's
  * mistake: their later rows are left unwritten).
  * A NaN among the codes and scales of the tokens that a row sees makes the row NaN (a V code: that value of

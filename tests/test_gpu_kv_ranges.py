@@ -115,3 +115,25 @@ def test_attention_nan_scales_in_parts_of_cut_blocks(which, pages):
     ws = moe.alloc_kv_attention_workspace(Hq, Hkv, D, add)
     got = moe.kv_attention(q, device_cache(codes, scale), t.block_table, t.kv_len, t.tok_start, ws, max_q=add)
     assert torch.isnan(got[:, :4].float()).all() and torch.isfinite(got[:, 4:].float()).all()
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("k_exp", [0, -30])
+@pytest.mark.parametrize("Hq,add", [(4, 1), (24, 1), (4, 130)])
+def test_attention_query_that_is_not_finite(Hq, add, k_exp, value):
+    """A row of q with an infinity or a NaN has no softmax: it is NaN, whatever the size of K, and no other row
+    is touched."""
+    rng = np.random.default_rng(Hq)
+    D = 128
+    q, _, _, codes, scale, t = attention_case(rng, [500], [add], 16, Hq, 1, D)
+    scale = scale.copy()
+    scale[0] *= 2.0 ** k_exp
+    cache = device_cache(codes, scale)
+    ws = moe.alloc_kv_attention_workspace(Hq, 1, D, add)
+    call = lambda: moe.kv_attention(q, cache, t.block_table, t.kv_len, t.tok_start, ws, max_q=add)  # noqa: E731
+    plain = call()
+    q[add // 2, 1, 77] = value
+    got = call()
+    assert torch.isnan(got[add // 2, 1].float()).all()
+    got[add // 2, 1] = plain[add // 2, 1]
+    assert torch.equal(got, plain)
