@@ -108,7 +108,8 @@ __global__ void __launch_bounds__(kTabThreads) k_kv_tables(const moe_kv_tables_a
       const bool fits = want[j] <= W * P;
       const int d = fits ? pages(want[j]) - pages(cur[j]) : 0;
       const int need = max(d, 0);
-      const bool ok = fits && (need == 0 || at.need + need <= count1);
+      const int add = fits ? max(want[j] - cur[j], 0) : 0;
+      const bool ok = fits && (need == 0 || at.need + need <= count1) && (add == 0 || at.tok + add <= a.max_tokens);
       rel_at[i] = at.rel;
       need_at[i] = at.need;
       tok_at[i] = at.tok;
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(kTabThreads) k_kv_tables(const moe_kv_tables_a
       run_at[i] = runs;            // within this thread, for now
       at.rel += max(-d, 0);
       at.need += need;
-      if (fits) at.tok += max(want[j] - cur[j], 0);
+      at.tok += add;
       refused += ok ? 0 : 1;
       granted += ok ? need : 0;
       if (ok && want[j] > cur[j]) runs += ((want[j] - 1) >> shift) - (cur[j] >> shift) + 1;

@@ -277,7 +277,8 @@ class PagedAttention:
     another stream, ordered after the step before it) while kernels of that step still read the first.
 
     rope: rope_table's result or None; max_tokens: capacity of a step's added tokens (q, k and v always
-    have that many rows; rows past a step's tokens are ignored); max_q: most tokens a request adds at once.
+    have that many rows; rows past a step's tokens are ignored); max_q: most tokens a request adds at once
+    (of more than that only the first max_q get an output).
     """
 
     def __init__(self, *, num_layers: int, num_pages: int, page_size: int, num_heads: int, num_kv_heads: int,
@@ -294,7 +295,8 @@ class PagedAttention:
 
     def advance(self, new_len, stream=None) -> KVTables:
         """Take every request to new_len cached tokens (int32 device tensor; 0: finished).  tables.info says
-        on the device how many tokens were added and how many requests the pool refused."""
+        on the device how many tokens were added and how many requests were refused, because the pool or
+        max_tokens did not suffice: those keep the length they had."""
         t = self.tables
         kv_tables(t.kv_len, new_len, t.block_table, t.free_list, t.free_count, page_size=self.page_size,
                   out=self._next, stream=stream)

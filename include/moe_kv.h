@@ -34,10 +34,13 @@ extern "C" {
  *    pages are refused too (a request that needs none never is).  The granted pages are the topmost
  *    entries of the stack, handed out in stored order, so growing and giving back restores the stack.
  *  - A request whose new_len exceeds max_pages * page_size is refused and adds no tokens.
+ *  - While the added tokens so far fit max_tokens; once a request's do not, it and later requests that
+ *    add tokens are refused (their tokens are counted all the same: info[0] above max_tokens shows it).
  *  - kv_len[b] = new_len[b], or cur_len[b] for a refused request.
  *  - The added tokens of all requests are numbered in request order: those of request b are
  *    [tok_start[b], tok_start[b+1]).  Token t: request[t] = b, position[t] = its place in the
- *    request, slot[t] = page * page_size + row, or -1 when the request was refused.  Entries from the
+ *    request, slot[t] = page * page_size + row, or -1 when the request was refused (nothing is written to the
+ *    cache for it, and its rows of the attention's output hold nothing of use).  Entries from the
  *    total up to max_tokens read slot -1, position 0, request -1 (a captured graph can run on them).
  *  - A run is the added tokens of one request that share a page: run r is tokens
  *    [run_tok[r], run_tok[r] + run_len[r]); unused entries are 0, 0.

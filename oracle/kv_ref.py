@@ -31,10 +31,12 @@ def kv_tables(cur_len, new_len, block_table, free_list, free_count, P, max_token
                     free[count] = int(table[b, j])
                 count += 1
     needs = [max(0, pages(w, P) - pages(c, P)) if f else 0 for c, w, f in zip(cur, want, fits)]
-    total, ok = 0, []
+    total, tokens, ok = 0, 0, []
     for b in range(B):
         total += needs[b]
-        ok.append(fits[b] and (needs[b] == 0 or total <= count))
+        add = max(0, want[b] - cur[b]) if fits[b] else 0
+        tokens += add
+        ok.append(fits[b] and (needs[b] == 0 or total <= count) and (add == 0 or tokens <= max_tokens))
     granted = sum(n for n, o in zip(needs, ok) if o)
     top = free[count - granted:count]
     out = np.full((B, W), -1, np.int64)
