@@ -22,6 +22,29 @@ static moe_status check_cache(int Hkv, int D, int page_size, int num_pages) {
 
 static bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }
 
+// Whether an output of the tables shares memory with an input.  Every CTA reads the inputs
+// for itself while others already write, so what is updated in place would differ from CTA to CTA.
+static bool tables_overlap(const moe_kv_tables_args& a) {
+  struct Range {
+    const int32_t* p;
+    long long n;
+  };
+  const long long B = a.B, cells = B * a.max_pages;
+  constexpr int kOut = 11;
+  const Range r[] = {{a.out_block_table, cells}, {a.out_free_list, a.num_pages}, {a.out_free_count, 1},
+                     {a.kv_len, B}, {a.tok_start, B + 1}, {a.slot, a.max_tokens}, {a.position, a.max_tokens},
+                     {a.request, a.max_tokens}, {a.run_tok, a.max_runs}, {a.run_len, a.max_runs}, {a.info, 4},
+                     {a.cur_len, B}, {a.new_len, B}, {a.block_table, cells}, {a.free_list, a.num_pages},
+                     {a.free_count, 1}};
+  constexpr int kAll = sizeof(r) / sizeof(r[0]);
+  for (int i = 0; i < kOut; ++i)
+    for (int j = kOut; j < kAll; ++j) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(r[i].p), y = reinterpret_cast<uintptr_t>(r[j].p);
+      if (r[i].n > 0 && r[j].n > 0 && x < y + 4 * r[j].n && y < x + 4 * r[i].n) return true;
+    }
+  return false;
+}
+
 // The workspace: status and counters, the prompts' plan, and parts, which the two kernels need one after the other.
 struct AttentionSpace {
   size_t plan, parts, total;
@@ -58,9 +81,7 @@ moe_status moe_kv_tables(const moe_kv_tables_args* a, moe_stream_t stream) {
   if (a->max_tokens > 0 && (!good(a->slot, 4) || !good(a->position, 4) || !good(a->request, 4)))
     return MOE_ERR_INVALID_ARG;
   if (a->max_runs > 0 && (!good(a->run_tok, 4) || !good(a->run_len, 4))) return MOE_ERR_INVALID_ARG;
-  if (a->out_block_table == a->block_table || a->out_free_count == a->free_count ||
-      (a->num_pages > 0 && a->out_free_list == a->free_list))
-    return MOE_ERR_INVALID_ARG;
+  if (tables_overlap(*a)) return MOE_ERR_INVALID_ARG;
   return launched(launch_kv_tables(*a, (cudaStream_t)stream));
 }
 

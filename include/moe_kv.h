@@ -47,6 +47,7 @@ extern "C" {
  *  - info = {added tokens, runs, refused requests, granted pages}.
  * Table entries past pages(kv_len[b]) are -1.  cur_len outside [0, max_pages * page_size] and a
  * negative new_len are clamped.
+ * No output may share memory with an input (kv_len is not cur_len): MOE_ERR_INVALID_ARG.
  * Supported: 1 <= B <= 4096, B * max_pages * page_size < 2^31.  max_runs must cover the runs:
  * min(max_tokens, max_tokens / page_size + 2 * B) always does (runs past max_runs are not listed). */
 typedef struct {
@@ -55,9 +56,9 @@ typedef struct {
   const int32_t* block_table;  /* [B, max_pages] */
   const int32_t* free_list;    /* [num_pages], the stack: entries [0, free_count) are free */
   const int32_t* free_count;   /* [1] */
-  int32_t* out_block_table;    /* [B, max_pages], not block_table itself */
-  int32_t* out_free_list;      /* [num_pages], not free_list itself */
-  int32_t* out_free_count;     /* [1], not free_count itself */
+  int32_t* out_block_table;    /* [B, max_pages] */
+  int32_t* out_free_list;      /* [num_pages] */
+  int32_t* out_free_count;     /* [1] */
   int32_t* kv_len;             /* [B] */
   int32_t* tok_start;          /* [B + 1] */
   int32_t* slot;               /* [max_tokens] */

@@ -1,8 +1,12 @@
 """The paged cache's capacities and argument checks, without a GPU: the CPU statement by hand, refusals on
 the host."""
 
-import numpy as np
+import ctypes
 
+import numpy as np
+import pytest
+
+import block_fp8_mixture_gb300 as moe
 from oracle import kv_ref
 
 
@@ -21,3 +25,33 @@ def test_tables_refuse_what_does_not_fit_the_token_list():
     assert t["run_len"].tolist() == [16, 4, 0, 0, 0, 0, 0, 0]
     u = kv_ref.kv_tables(t["kv_len"], [20, 17, 16, 1, 4, 5], t["block_table"], t["free_list"], 5, 16, 32, 8)
     assert u["kv_len"].tolist() == [20, 17, 16, 1, 4, 5] and u["info"].tolist() == [20, 4, 0, 3]
+
+
+# Arguments of a tables call whose buffers lie apart: fake device addresses, refused before anything uses them.
+TABLES = dict(B=4, max_pages=8, num_pages=64, page_size=16, max_tokens=32, max_runs=8)
+BUFFERS = ("cur_len", "new_len", "block_table", "free_list", "free_count", "out_block_table", "out_free_list",
+           "out_free_count", "kv_len", "tok_start", "slot", "position", "request", "run_tok", "run_len", "info")
+SIZES = dict(cur_len=4, new_len=4, block_table=32, free_list=64, free_count=1, out_block_table=32, out_free_list=64,
+             out_free_count=1, kv_len=4, tok_start=5, slot=32, position=32, request=32, run_tok=8, run_len=8, info=4)
+
+
+def tables_args(**kw):
+    where = {n: (i + 1) << 12 for i, n in enumerate(BUFFERS)}
+    return moe.KVTablesArgs(**{**TABLES, **where, **kw})
+
+
+@pytest.mark.parametrize("out", BUFFERS[5:])
+def test_tables_refuse_outputs_that_share_memory_with_inputs(lib, out):
+    """With every input: the same address, its last entry, and its first entry as the output's last."""
+    where = {n: getattr(tables_args(), n) for n in BUFFERS}
+    for other in BUFFERS[:5]:
+        for at in (where[other], where[other] + 4 * (SIZES[other] - 1), where[other] - 4 * (SIZES[out] - 1)):
+            args = tables_args(**{out: at})
+            assert lib.moe_kv_tables(ctypes.byref(args), None) == moe.MOE_ERR_INVALID_ARG, (out, other, at)
+
+
+@pytest.mark.parametrize("name", BUFFERS)
+def test_tables_refuse_missing_and_misaligned_buffers(lib, name):
+    for at in (None, getattr(tables_args(), name) + 2):
+        args = tables_args(**{name: at})
+        assert lib.moe_kv_tables(ctypes.byref(args), None) == moe.MOE_ERR_INVALID_ARG, at
