@@ -1,6 +1,8 @@
 """Binding of include/moe_kv.h: the paged 8-bit key/value cache, its tables, the rotary write and the
 attention that reads it.  As in the rest of the package these functions only marshal arguments; the
-work is done by the library's CUDA kernels on `stream` (default: torch's current stream).
+work is done by the library's CUDA kernels on `stream` (default: torch's current stream).  What a call
+allocates is allocated on that stream too, so that its memory is not handed out again while the kernels use it;
+as everywhere in torch, a tensor that another stream uses needs record_stream before it is dropped.
 """
 
 from __future__ import annotations
@@ -103,6 +105,16 @@ def _stream(stream):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+def _allocate(stream, make, *args, **kw):
+    """make(...) with the call's stream as torch's current one."""
+    if stream is None:
+        return make(*args, **kw)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _bad(what: str):
     raise MoeError(MOE_ERR_INVALID_ARG, what)
 
@@ -151,7 +163,7 @@ def kv_tables(cur_len, new_len, block_table, free_list, free_count, *, page_size
     if out is None:
         if max_tokens is None:
             _bad("kv_tables: max_tokens or out is needed")
-        out = alloc_kv_tables(B, W, N, page_size, max_tokens, block_table.device)
+        out = _allocate(stream, alloc_kv_tables, B, W, N, page_size, max_tokens, block_table.device)
     T, R = out.slot.shape[0], out.run_tok.shape[0]
     if max_tokens is not None and max_tokens != T:
         _bad("kv_tables: out holds another number of tokens than max_tokens")
@@ -174,7 +186,7 @@ def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, *, scaling: in
                magnitude: float = 1.0, out=None, device="cuda", stream=None):
     """cos and sin of every position, fp32 [max_pos, rot_dim / 2, 2] (moe_rope_table)."""
     if out is None:
-        out = torch.empty((max_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
+        out = _allocate(stream, torch.empty, (max_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
     elif out.dtype != torch.float32 or tuple(out.shape) != (max_pos, rot_dim // 2, 2) or not out.is_contiguous():
         _bad("rope_table: out is a contiguous fp32 tensor [max_pos, rot_dim / 2, 2]")
     _check(load_library().moe_rope_table(out.data_ptr(), max_pos, rot_dim, base, scaling, factor, low,
@@ -222,7 +234,7 @@ def rope_append(q, k, v, rope, tables: KVTables, cache: KVCache, *, layout: int 
     if q is not None:
         Hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+            q_out = _allocate(stream, torch.empty, (T, Hq, D), dtype=torch.bfloat16, device=q.device)
         qp, qt, qh = _heads("q", q, T, Hq, D)
         op, ot, oh = _heads("q_out", q_out, T, Hq, D)
     kp, kt, kh = _heads("k", k, T, Hkv, D)
@@ -257,7 +269,7 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, tok_start, workspace, *
     T, Hq = q.shape[0], q.shape[1]
     B, W = block_table.shape
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = _allocate(stream, torch.empty, (T, Hq, D), dtype=torch.bfloat16, device=q.device)
     qp, qt, qh = _heads("q", q, T, Hq, D)
     op, ot, oh = _heads("out", out, T, Hq, D)
     b = (B,)
@@ -274,7 +286,8 @@ class PagedAttention:
     """Rotary embedding, 8-bit paged cache and attention of a model's layers, for up to `max_requests`
     requests at a time.  The layers share the tables, which advance() moves one step on; each layer has
     its own cache.  Steps are built in the second of two sets of tables, so advance() may be called (on
-    another stream, ordered after the step before it) while kernels of that step still read the first.
+    another stream, ordered after the step before it) while kernels of that step still read the first.  The
+    object itself is made on the current stream: a first step on another one has to wait for that.
 
     rope: rope_table's result or None; max_tokens: capacity of a step's added tokens (q, k and v always
     have that many rows; rows past a step's tokens are ignored); max_q: most tokens a request adds at once
