@@ -94,15 +94,19 @@ class KVCache(NamedTuple):
     v_scale: object
 
 
-def _stream(stream):
-    """The stream's handle; torch's current one through the raw handle, without building an object
-    (3 us of a call that takes 10)."""
+def _stream(stream, dev: int):
+    """The stream's handle, for tensors on device `dev`, which has to be the current one; torch's current
+    stream through the raw handle, without building an object (3 us of a call that takes 10)."""
+    if dev != _current_device():
+        _bad(f"the tensors are on device {dev}, the current device is {_current_device()}")
     if stream is None and _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(dev)
     return _given_stream(stream)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# (there are tensors on a device when this is asked, so torch need not look whether CUDA is initialised)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _allocate(stream, make, *args, **kw):
@@ -119,9 +123,17 @@ def _bad(what: str):
     raise MoeError(MOE_ERR_INVALID_ARG, what)
 
 
-def _i32(name: str, t, shape):
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
-        _bad(f"{name}: a contiguous int32 tensor of shape {shape} is needed")
+def _device(name: str, t) -> int:
+    """The CUDA device that a call's first tensor is on, and so all others have to be."""
+    dev = t.get_device()
+    if dev < 0:
+        _bad(f"{name}: a CUDA tensor is needed")
+    return dev
+
+
+def _i32(name: str, t, shape, dev: int):
+    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _bad(f"{name}: a contiguous int32 tensor of shape {shape} on device {dev} is needed")
     return t.data_ptr()
 
 
@@ -164,20 +176,22 @@ def kv_tables(cur_len, new_len, block_table, free_list, free_count, *, page_size
         if max_tokens is None:
             _bad("kv_tables: max_tokens or out is needed")
         out = _allocate(stream, alloc_kv_tables, B, W, N, page_size, max_tokens, block_table.device)
-    T, R = out.slot.shape[0], out.run_tok.shape[0]
+    o_table, o_free, o_count, kv_len, tok_start, slot, position, request, run_tok, run_len, info = out
+    T, R = slot.shape[0], run_tok.shape[0]
     if max_tokens is not None and max_tokens != T:
         _bad("kv_tables: out holds another number of tokens than max_tokens")
+    d = _device("block_table", block_table)
     b, t, r, one, table, pool = (B,), (T,), (R,), (1,), (B, W), (N,)
     a = _PACK_TABLES.pack(
-        _i32("cur_len", cur_len, b), _i32("new_len", new_len, b), _i32("block_table", block_table, table),
-        _i32("free_list", free_list, pool), _i32("free_count", free_count, one),
-        _i32("out.block_table", out.block_table, table), _i32("out.free_list", out.free_list, pool),
-        _i32("out.free_count", out.free_count, one), _i32("out.kv_len", out.kv_len, b),
-        _i32("out.tok_start", out.tok_start, (B + 1,)), _i32("out.slot", out.slot, t),
-        _i32("out.position", out.position, t), _i32("out.request", out.request, t),
-        _i32("out.run_tok", out.run_tok, r), _i32("out.run_len", out.run_len, r),
-        _i32("out.info", out.info, (4,)), B, W, N, page_size, T, R)
-    _check(load_library().moe_kv_tables(a, _stream(stream)), "moe_kv_tables")
+        _i32("cur_len", cur_len, b, d), _i32("new_len", new_len, b, d), _i32("block_table", block_table, table, d),
+        _i32("free_list", free_list, pool, d), _i32("free_count", free_count, one, d),
+        _i32("out.block_table", o_table, table, d), _i32("out.free_list", o_free, pool, d),
+        _i32("out.free_count", o_count, one, d), _i32("out.kv_len", kv_len, b, d),
+        _i32("out.tok_start", tok_start, (B + 1,), d), _i32("out.slot", slot, t, d),
+        _i32("out.position", position, t, d), _i32("out.request", request, t, d),
+        _i32("out.run_tok", run_tok, r, d), _i32("out.run_len", run_len, r, d),
+        _i32("out.info", info, (4,), d), B, W, N, page_size, T, R)
+    _check(load_library().moe_kv_tables(a, _stream(stream, d)), "moe_kv_tables")
     return out
 
 
@@ -190,15 +204,15 @@ def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, *, scaling: in
     elif out.dtype != torch.float32 or tuple(out.shape) != (max_pos, rot_dim // 2, 2) or not out.is_contiguous():
         _bad("rope_table: out is a contiguous fp32 tensor [max_pos, rot_dim / 2, 2]")
     _check(load_library().moe_rope_table(out.data_ptr(), max_pos, rot_dim, base, scaling, factor, low,
-                                         high, original_len, magnitude, _stream(stream)),
+                                         high, original_len, magnitude, _stream(stream, _device("out", out))),
            "moe_rope_table")
     return out
 
 
-def _heads(name: str, t, T: int, H: int, D: int):
+def _heads(name: str, t, T: int, H: int, D: int, dev: int):
     """Pointer, token stride and head stride of a BF16 tensor [T, H, D] with contiguous heads."""
-    if t.dtype is not torch.bfloat16 or t.shape != (T, H, D):
-        _bad(f"{name}: a bfloat16 tensor of shape {(T, H, D)} is needed")
+    if t.dtype is not torch.bfloat16 or t.shape != (T, H, D) or t.get_device() != dev:
+        _bad(f"{name}: a bfloat16 tensor of shape {(T, H, D)} on device {dev} is needed")
     st, sh, sd = t.stride()
     if sd != 1:
         _bad(f"{name}: the values of a head have to be contiguous")
@@ -206,15 +220,19 @@ def _heads(name: str, t, T: int, H: int, D: int):
 
 
 def _cache(cache: KVCache):
-    """Pointers of the cache's tensors and (num_pages, Hkv, page_size, D)."""
+    """Pointers of the cache's tensors, (num_pages, Hkv, page_size, D) and the device."""
     kc, vc, ks, vs = cache
     shape = kc.shape
+    dev = _device("cache", kc)
     if (len(shape) != 4 or vc.shape != shape or kc.element_size() != 1 or vc.element_size() != 1
             or ks.shape != shape[:2] or vs.shape != ks.shape or ks.dtype is not torch.float32
-            or vs.dtype is not torch.float32 or not (kc.is_contiguous() and vc.is_contiguous()
-                                                     and ks.is_contiguous() and vs.is_contiguous())):
-        _bad("cache: contiguous codes [num_pages, Hkv, page_size, D] and fp32 scales [num_pages, Hkv] are needed")
-    return kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape
+            or vs.dtype is not torch.float32
+            or not (vc.get_device() == ks.get_device() == vs.get_device() == dev)
+            or not (kc.is_contiguous() and vc.is_contiguous()
+                    and ks.is_contiguous() and vs.is_contiguous())):
+        _bad("cache: contiguous codes [num_pages, Hkv, page_size, D] and fp32 scales [num_pages, Hkv] "
+             "on one device are needed")
+    return kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape, dev
 
 
 def rope_append(q, k, v, rope, tables: KVTables, cache: KVCache, *, layout: int = ROPE_HALF,
@@ -222,29 +240,30 @@ def rope_append(q, k, v, rope, tables: KVTables, cache: KVCache, *, layout: int 
     """Rotate q and k [T, heads, D] by the tables' positions, write k and v to the cache and return the
     rotated q (moe_rope_append).  rope: rope_table's result, or None for no rotation; q None: cache
     write only; q_out may be q.  T is the tables' token capacity."""
-    kc, vc, ks, vs, (N, Hkv, P, D) = _cache(cache)
+    kc, vc, ks, vs, (N, Hkv, P, D), d = _cache(cache)
     T, R = tables.slot.shape[0], tables.run_tok.shape[0]
     rot = max_pos = 0
     rp = 0
     if rope is not None:
-        if rope.dtype is not torch.float32 or rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous():
-            _bad("rope: a contiguous fp32 tensor [max_pos, rot_dim / 2, 2] is needed")
+        if (rope.dtype is not torch.float32 or rope.dim() != 3 or rope.shape[2] != 2 or rope.get_device() != d
+                or not rope.is_contiguous()):
+            _bad(f"rope: a contiguous fp32 tensor [max_pos, rot_dim / 2, 2] on device {d} is needed")
         max_pos, rot, rp = rope.shape[0], 2 * rope.shape[1], rope.data_ptr()
     Hq = qp = op = qt = qh = ot = oh = 0
     if q is not None:
         Hq = q.shape[1]
         if q_out is None:
             q_out = _allocate(stream, torch.empty, (T, Hq, D), dtype=torch.bfloat16, device=q.device)
-        qp, qt, qh = _heads("q", q, T, Hq, D)
-        op, ot, oh = _heads("q_out", q_out, T, Hq, D)
-    kp, kt, kh = _heads("k", k, T, Hkv, D)
-    vp, vt, vh = _heads("v", v, T, Hkv, D)
+        qp, qt, qh = _heads("q", q, T, Hq, D, d)
+        op, ot, oh = _heads("q_out", q_out, T, Hq, D, d)
+    kp, kt, kh = _heads("k", k, T, Hkv, D, d)
+    vp, vt, vh = _heads("v", v, T, Hkv, D, d)
     t, r = (T,), (R,)
-    a = _PACK_APPEND.pack(qp, kp, vp, op, rp, _i32("position", tables.position, t),
-                          _i32("slot", tables.slot, t), _i32("run_tok", tables.run_tok, r),
-                          _i32("run_len", tables.run_len, r), kc, vc, ks, vs, qt, qh, kt, kh, vt, vh,
+    a = _PACK_APPEND.pack(qp, kp, vp, op, rp, _i32("position", tables.position, t, d),
+                          _i32("slot", tables.slot, t, d), _i32("run_tok", tables.run_tok, r, d),
+                          _i32("run_len", tables.run_len, r, d), kc, vc, ks, vs, qt, qh, kt, kh, vt, vh,
                           ot, oh, T, Hq, Hkv, D, P, N, R, rot, max_pos, layout, scale_fmt)
-    _check(load_library().moe_rope_append(a, _stream(stream)), "moe_rope_append")
+    _check(load_library().moe_rope_append(a, _stream(stream, d)), "moe_rope_append")
     return q_out
 
 
@@ -265,19 +284,21 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, tok_start, workspace, *
     rows [tok_start[b], tok_start[b+1]) of q and the last ones of its kv_len[b] cached tokens.  max_q
     bounds the tokens of one request; sm_scale defaults to D^-0.5; window > 0 limits how far back a
     token sees."""
-    kc, vc, ks, vs, (N, Hkv, P, D) = _cache(cache)
+    kc, vc, ks, vs, (N, Hkv, P, D), d = _cache(cache)
     T, Hq = q.shape[0], q.shape[1]
     B, W = block_table.shape
     if out is None:
         out = _allocate(stream, torch.empty, (T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    qp, qt, qh = _heads("q", q, T, Hq, D)
-    op, ot, oh = _heads("out", out, T, Hq, D)
+    qp, qt, qh = _heads("q", q, T, Hq, D, d)
+    op, ot, oh = _heads("out", out, T, Hq, D, d)
+    if workspace.get_device() != d or not workspace.is_contiguous():
+        _bad(f"workspace: a contiguous tensor on device {d} is needed")
     b = (B,)
-    a = _PACK_ATTENTION.pack(qp, kc, vc, ks, vs, _i32("block_table", block_table, (B, W)),
-                             _i32("kv_len", kv_len, b), _i32("tok_start", tok_start, (B + 1,)), op, qt, qh,
+    a = _PACK_ATTENTION.pack(qp, kc, vc, ks, vs, _i32("block_table", block_table, (B, W), d),
+                             _i32("kv_len", kv_len, b, d), _i32("tok_start", tok_start, (B + 1,), d), op, qt, qh,
                              ot, oh, T, B, Hq, Hkv, D, P, N, W, max_q, window,
                              1.0 / math.sqrt(D) if sm_scale is None else sm_scale)
-    _check(load_library().moe_kv_attention(a, workspace.data_ptr(), workspace.numel(), _stream(stream)),
+    _check(load_library().moe_kv_attention(a, workspace.data_ptr(), workspace.numel(), _stream(stream, d)),
            "moe_kv_attention")
     return out
 

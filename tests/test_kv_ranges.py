@@ -55,3 +55,26 @@ def test_tables_refuse_missing_and_misaligned_buffers(lib, name):
     for at in (None, getattr(tables_args(), name) + 2):
         args = tables_args(**{name: at})
         assert lib.moe_kv_tables(ctypes.byref(args), None) == moe.MOE_ERR_INVALID_ARG, at
+
+
+def test_binding_refuses_tensors_of_the_host(lib):
+    """Tensors in host memory, right in all else: refused before their addresses reach the library."""
+    torch = pytest.importorskip("torch")
+    cache = moe.alloc_kv_cache(4, 2, 16, 64, device="cpu")
+    t = moe.alloc_kv_tables(2, 4, 4, 16, 8, device="cpu")
+    q = torch.zeros(8, 4, 64, dtype=torch.bfloat16)
+    kv = torch.zeros(8, 2, 64, dtype=torch.bfloat16)
+    ws = torch.zeros(moe.kv_attention_workspace_bytes(4, 2, 64, 8), dtype=torch.uint8)
+    attn = moe.PagedAttention(num_layers=1, num_pages=4, page_size=16, num_heads=4, num_kv_heads=2, head_dim=64,
+                              max_requests=2, max_pages=4, max_tokens=8, max_q=8, device="cpu")
+    for call in (
+            lambda: moe.kv_tables(t.kv_len, t.kv_len, t.block_table, t.free_list, t.free_count, page_size=16,
+                                  max_tokens=8),
+            lambda: moe.rope_table(16, 32, device="cpu"),
+            lambda: moe.rope_append(q, kv, kv, None, t, cache),
+            lambda: moe.kv_attention(q, cache, t.block_table, t.kv_len, t.tok_start, ws, max_q=8),
+            lambda: attn.advance(t.kv_len),
+            lambda: attn(0, q, kv, kv)):
+        with pytest.raises(moe.MoeError) as e:
+            call()
+        assert e.value.status == moe.MOE_ERR_INVALID_ARG
