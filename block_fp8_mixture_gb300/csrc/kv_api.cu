@@ -143,10 +143,10 @@ moe_status moe_kv_attention(const moe_kv_attention_args* a, void* workspace, siz
   const moe_status st = check_cache(a->Hkv, a->D, a->page_size, a->num_pages);
   if (st != MOE_OK) return st;
   if (a->Hq % a->Hkv || a->Hq / a->Hkv > kMaxGroup || a->B > kMaxRequests ||
-      (long long)a->max_pages * a->page_size > 0x7FFFFFFFll)
+      (long long)a->max_pages * a->page_size > 0x80000000ll - kTileTokens)   // tiles end within 32 bits
     return MOE_ERR_UNSUPPORTED_SHAPE;
   // shares of the few-row kernel's tiles are counted in 32 bits
-  if (((long long)a->B * a->max_pages * a->page_size / 128 + 4ll * a->B) * a->Hkv > 0x7FFFFFFFll - (1 << 20))
+  if (((long long)a->B * a->max_pages * a->page_size / kTileTokens + 4ll * a->B) * a->Hkv > 0x7FFFFFFFll - (1 << 20))
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!(a->sm_scale > 0.0f) || !isfinite(a->sm_scale)) return MOE_ERR_INVALID_ARG;
   if (!good(workspace, 256)) return MOE_ERR_INVALID_ARG;

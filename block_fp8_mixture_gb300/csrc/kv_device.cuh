@@ -7,7 +7,7 @@
 
 namespace moe {
 
-constexpr int kTile = 128;                 // tokens per tile
+constexpr int kTile = kTileTokens;         // tokens per tile
 constexpr int kMaxTilePages = 8;           // pages of a tile, at page size 16
 constexpr float kLog2e = 1.4426950408889634f;
 

@@ -8,6 +8,7 @@ namespace moe {
 
 constexpr int kMaxRequests = 4096;
 constexpr int kMaxGroup = 64;          // query heads per key/value head
+constexpr int kTileTokens = 128;       // cached tokens that the attention kernels take at a time
 
 cudaError_t launch_kv_tables(const moe_kv_tables_args& a, cudaStream_t s);
 cudaError_t launch_rope_table(float* table, int max_pos, int rot, double base, int scaling,

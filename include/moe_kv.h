@@ -147,7 +147,7 @@ moe_status moe_rope_append(const moe_rope_append_args* args, moe_stream_t stream
  * Parts of a long request are kept in the workspace on the way: FP32 with few query rows, FP32
  * without the last 8 bits (with whole FP32 statistics) with many: 2^-15, where the rounding of out is 2^-8.
  * MOE_ERR_INVALID_ARG with num_pages 0; MOE_ERR_UNSUPPORTED_SHAPE where the work would pass 32-bit counts:
- * T * (Hq / Hkv) / 512 + B > 65536 with more rows than 64 in a request, or
+ * max_pages * page_size > 2^31 - 128, T * (Hq / Hkv) / 512 + B > 65536 with more rows than 64 in a request, or
  * Hkv * (B * max_pages * page_size / 128 + 4 * B) >= 2^31 - 2^20.
  * The workspace (256-byte aligned) starts with the int32 status word that moe_last_device_status
  * reads; the caller zeroes the workspace once after allocating it, and again after a call whose status

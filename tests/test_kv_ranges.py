@@ -78,3 +78,14 @@ def test_binding_refuses_tensors_of_the_host(lib):
         with pytest.raises(moe.MoeError) as e:
             call()
         assert e.value.status == moe.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("page_size", [16, 32, 64])
+def test_attention_refuses_caches_whose_last_tile_passes_32_bits(lib, page_size):
+    at = {n: (i + 1) << 12 for i, n in enumerate(("q", "k_codes", "v_codes", "k_scale", "v_scale", "block_table",
+                                                  "kv_len", "tok_start", "out"))}
+    need = lib.moe_kv_attention_workspace_bytes(4, 1, 128, 1)
+    a = moe.KVAttentionArgs(**at, q_token_stride=512, q_head_stride=128, out_token_stride=512, out_head_stride=128,
+                            T=4, B=1, Hq=4, Hkv=1, D=128, page_size=page_size, num_pages=64,
+                            max_pages=(2 ** 31 - 128) // page_size + 1, max_q=1, window=0, sm_scale=0.1)
+    assert lib.moe_kv_attention(ctypes.byref(a), 1 << 20, need, None) == moe.MOE_ERR_UNSUPPORTED_SHAPE
