@@ -72,6 +72,8 @@ moe_status moe_kv_tables(const moe_kv_tables_args* a, moe_stream_t stream) {
   if (a->B > kMaxRequests || (long long)a->B * a->max_pages * a->page_size > 0x7FFFFFFFll ||
       (long long)a->num_pages * a->page_size > 0x7FFFFFFFll)
     return MOE_ERR_UNSUPPORTED_SHAPE;
+  // a stride of the grid past the end stays within 32 bits
+  if (a->max_tokens > kMaxList || a->max_runs > kMaxList) return MOE_ERR_UNSUPPORTED_SHAPE;
   const void* need[] = {a->cur_len, a->new_len, a->block_table, a->free_count, a->out_block_table,
                         a->out_free_count, a->kv_len, a->tok_start, a->info};
   for (const void* p : need)

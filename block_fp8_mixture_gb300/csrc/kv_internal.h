@@ -7,6 +7,7 @@
 namespace moe {
 
 constexpr int kMaxRequests = 4096;
+constexpr int kMaxList = 0x7FFFFFFF - (1 << 20);   // entries of a step's token or run list
 constexpr int kMaxGroup = 64;          // query heads per key/value head
 constexpr int kTileTokens = 128;       // cached tokens that the attention kernels take at a time
 

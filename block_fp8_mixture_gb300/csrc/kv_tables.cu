@@ -14,6 +14,8 @@ namespace moe {
 constexpr int kTabThreads = 512;
 constexpr int kTabItems = kMaxRequests / kTabThreads;   // requests per thread, at most
 constexpr int kTabPerThread = 4;                        // output entries per thread that size the grid
+constexpr int kTabCtas = 304;                           // at most
+static_assert((long long)kMaxList + kTabCtas * kTabThreads <= 0x7FFFFFFF, "the loops' counters");
 
 struct Scan3 {
   int rel, need, tok;
@@ -206,7 +208,7 @@ cudaError_t launch_kv_tables(const moe_kv_tables_args& a, cudaStream_t s) {
   }
   const long long out = (long long)a.B * a.max_pages + a.num_pages + a.max_tokens + a.max_runs;
   const long long want = (out + kTabThreads * kTabPerThread - 1) / (kTabThreads * kTabPerThread);
-  const int grid = (int)(want < 1 ? 1 : want > 304 ? 304 : want);
+  const int grid = (int)(want < 1 ? 1 : want > kTabCtas ? kTabCtas : want);
   k_kv_tables<<<grid, kTabThreads, smem, s>>>(a);
   return cudaGetLastError();
 }

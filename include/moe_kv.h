@@ -48,7 +48,8 @@ extern "C" {
  * Table entries past pages(kv_len[b]) are -1.  cur_len outside [0, max_pages * page_size] and a
  * negative new_len are clamped.
  * No output may share memory with an input (kv_len is not cur_len): MOE_ERR_INVALID_ARG.
- * Supported: 1 <= B <= 4096, B * max_pages * page_size < 2^31.  max_runs must cover the runs:
+ * Supported: 1 <= B <= 4096, B * max_pages * page_size < 2^31, max_tokens and max_runs below 2^31 - 2^20.
+ * max_runs must cover the runs:
  * min(max_tokens, max_tokens / page_size + 2 * B) always does (runs past max_runs are not listed). */
 typedef struct {
   const int32_t* cur_len;      /* [B] */

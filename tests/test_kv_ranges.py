@@ -89,3 +89,10 @@ def test_attention_refuses_caches_whose_last_tile_passes_32_bits(lib, page_size)
                             T=4, B=1, Hq=4, Hkv=1, D=128, page_size=page_size, num_pages=64,
                             max_pages=(2 ** 31 - 128) // page_size + 1, max_q=1, window=0, sm_scale=0.1)
     assert lib.moe_kv_attention(ctypes.byref(a), 1 << 20, need, None) == moe.MOE_ERR_UNSUPPORTED_SHAPE
+
+
+@pytest.mark.parametrize("name", ["max_tokens", "max_runs"])
+def test_tables_refuse_lists_whose_loops_pass_32_bits(lib, name):
+    far = {n: (i + 1) << 40 for i, n in enumerate(BUFFERS)}
+    args = tables_args(**far, **{name: 2 ** 31 - 2 ** 20})
+    assert lib.moe_kv_tables(ctypes.byref(args), None) == moe.MOE_ERR_UNSUPPORTED_SHAPE
