@@ -108,6 +108,8 @@ moe_status moe_rope_append(const moe_rope_append_args* a, moe_stream_t stream) {
   const moe_status st = check_cache(a->Hkv, a->D, a->page_size, a->num_pages);
   if (st != MOE_OK) return st;
   if (a->rot_dim % 16 || a->rot_dim > a->D || a->Hq > 65536) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // the units of the cache's write (run, head, K or V) and the last block's spare ones are counted in 32 bits
+  if ((long long)a->max_runs * 2 * a->Hkv > 0xFFFFFFFFll - 8) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (a->layout < MOE_ROPE_HALF || a->layout > MOE_ROPE_INTERLEAVED) return MOE_ERR_INVALID_ARG;
   if (a->scale_fmt != MOE_SCALE_FP32 && a->scale_fmt != MOE_SCALE_FP32_POW2) return MOE_ERR_INVALID_ARG;
   if (a->T == 0) return MOE_OK;

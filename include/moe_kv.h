@@ -105,6 +105,7 @@ moe_status moe_rope_table(float* table, int max_pos, int rot_dim, double base, m
  * q_out may be q itself.  Strides are in elements, multiples of 8; values of a head are contiguous.
  * position[t] must be below max_pos (it is clamped).  rot_dim 0 (rope NULL): no rotation.
  * Infinite inputs saturate the page's scale; a NaN becomes the NaN code and does not enter amax.
+ * max_runs * 2 * Hkv < 2^32 - 8, else MOE_ERR_UNSUPPORTED_SHAPE.
  * scale_fmt: MOE_SCALE_FP32 or MOE_SCALE_FP32_POW2.  Hq may be 0 (q and q_out NULL): cache write only. */
 typedef struct {
   const void* q;           /* bf16 [T, Hq, D] */

@@ -96,3 +96,13 @@ def test_tables_refuse_lists_whose_loops_pass_32_bits(lib, name):
     far = {n: (i + 1) << 40 for i, n in enumerate(BUFFERS)}
     args = tables_args(**far, **{name: 2 ** 31 - 2 ** 20})
     assert lib.moe_kv_tables(ctypes.byref(args), None) == moe.MOE_ERR_UNSUPPORTED_SHAPE
+
+
+def test_append_refuses_more_units_than_32_bits_count(lib):
+    at = {n: (i + 1) << 40 for i, n in enumerate(("q", "k", "v", "q_out", "rope", "position", "slot", "run_tok",
+                                                  "run_len", "k_codes", "v_codes", "k_scale", "v_scale"))}
+    a = moe.RopeAppendArgs(**at, q_token_stride=512, q_head_stride=128, k_token_stride=131072, k_head_stride=128,
+                           v_token_stride=131072, v_head_stride=128, qo_token_stride=512, qo_head_stride=128, T=4,
+                           Hq=4, Hkv=1024, D=128, page_size=16, num_pages=64, max_runs=2 ** 21 + 1, rot_dim=128,
+                           max_pos=100, layout=0, scale_fmt=0)
+    assert lib.moe_rope_append(ctypes.byref(a), None) == moe.MOE_ERR_UNSUPPORTED_SHAPE
