@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kWPU == 8 ? 256 : 128)
   if (run >= (unsigned)a.max_runs) return;
   const int n = min(a.run_len[run], a.page_size);
   const int tok0 = a.run_tok[run];
-  if (n <= 0 || tok0 < 0 || tok0 + n > a.T) return;
+  if (n <= 0 || tok0 < 0 || tok0 > a.T - n) return;
   const int slot = a.slot[tok0];
   const int page = slot < 0 ? -1 : slot / a.page_size;
   if (page < 0 || page >= a.num_pages) return;

@@ -109,11 +109,12 @@ template <int kNR>
 __device__ __forceinline__ FewItem few_item(const FewParams& p, int b) {
   FewItem it;
   it.q0 = p.a.tok_start[b];
-  const int n = p.a.tok_start[b + 1] - it.q0;
+  const int q1 = p.a.tok_start[b + 1], n = q1 - it.q0;
   it.n = min(n, p.a.max_q);
   it.pos0 = min(max(p.a.kv_len[b], 0), p.a.max_pages << p.page_shift) - n;
   it.lo = it.hi = it.tile0 = it.tiles = 0;
-  if (n >= 1 && it.n <= kNR / p.G && it.q0 >= 0 && it.q0 + n <= p.a.T) {
+  // (comparisons only, so that no pair of entries passes by a difference that wraps round)
+  if (it.q0 >= 0 && q1 > it.q0 && q1 <= p.a.T && it.n <= kNR / p.G) {
     it.hi = max(0, it.pos0 + it.n);
     if (p.a.window > 0) it.lo = max(0, it.pos0 - p.a.window + 1);
     it.tile0 = it.lo / kTile;

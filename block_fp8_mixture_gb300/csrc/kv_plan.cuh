@@ -97,9 +97,9 @@ __device__ __forceinline__ void prompt_plan(const moe_kv_attention_args& a, cons
   const int threads = blockDim.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto blocks_of = [&](int b) {
-    const int q0 = a.tok_start[b], n = a.tok_start[b + 1] - q0;
-    if (n <= pl.min_n || q0 < 0 || q0 + n > a.T) return 0;
-    return (min(n, a.max_q) * G + kBlockRows - 1) / kBlockRows;
+    const int q0 = a.tok_start[b], q1 = a.tok_start[b + 1];
+    if (q0 < 0 || q1 <= q0 || q1 > a.T || q1 - q0 <= pl.min_n) return 0;
+    return (min(q1 - q0, a.max_q) * G + kBlockRows - 1) / kBlockRows;
   };
   auto scan = [&](int v) {                    // inclusive sum over the block
 #pragma unroll
