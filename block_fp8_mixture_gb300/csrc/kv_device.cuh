@@ -71,14 +71,6 @@ __device__ __forceinline__ void mma_f8_warp(uint32_t d_tmem, uint64_t a_desc, ui
                : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]: FP16 operands, fp32 sums.
-__device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                                uint32_t idesc, uint32_t accumulate) {
-  asm volatile(KV_ELECT "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-               "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-               : "memory");
-}
-
 // Arrive on `bar` when the elected lane's products so far are complete.
 __device__ __forceinline__ void mma_commit_warp(uint32_t bar) {
   asm volatile(

@@ -549,7 +549,6 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
         constexpr uint32_t kIdescO = make_idesc_e4m3(kD, 16 * C::PPieces) | (3u << 15);   // both MN-major
         const uint64_t qd = rows_desc<kD>(sQ), pd = p_desc<kNR>(sP);
         int segs = 0;
-        const bool ok = true;
         auto scores = [&](int it) {
           const int s = it % C::Stages;
           if (!mbar_wait_warp(kfull(s), (it / C::Stages) & 1, abort_flag, status)) return false;
@@ -561,7 +560,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
           mma_commit_warp(sfull(it & 1));
           return true;
         };
-        for (int it = 0; ok; ++it) {
+        for (int it = 0;; ++it) {
           const int s = it % C::Stages;
           if (it == 0) {
             if (!mbar_wait_warp(qfull, segs & 1, abort_flag, status) || !scores(0)) break;

@@ -25,7 +25,6 @@ constexpr int kBins = 1024;                   // lengths that the order tells ap
 constexpr int kPromptCtas = 152;              // at most (SMs)
 constexpr int kPromptPairs = kPromptCtas / 2;
 constexpr int kItemStart = 3;                 // units
-constexpr int kMinPart = 2;                   // tiles
 constexpr int kCutTiles = 12;                 // of the longest item of the last round, at least, for cuts
 
 // The last round: item i has units from start[i] on, pair c those from bound[c] on.
