@@ -211,13 +211,14 @@ __global__ void __launch_bounds__(kWPU == 8 ? 256 : 128)
   float s = group_scale(amax, a.scale_fmt);
   if (off > 0) s = fmaxf(s, was);
   if (ut == 0) *scale = s;
-  // x / s rounded once: two corrections of x (1/s) by the exact remainder (Markstein), for finite s
+  // x / s rounded once: two corrections of x (1/s) by the exact remainder (Markstein), for finite s.  The remainder
+  // is taken with the sign turned, q s - x: so a negative zero stays one.
   const bool finite = s <= 3.4e38f;
   const float inv = finite ? __frcp_rn(s) : 0.0f;
   auto quotient = [&](float x) {
     const float q0 = __fmul_rn(x, inv);
-    const float q1 = __fmaf_rn(__fmaf_rn(-s, q0, x), inv, q0);
-    return __fmaf_rn(__fmaf_rn(-s, q1, x), inv, q1);
+    const float q1 = __fmaf_rn(-__fmaf_rn(q0, s, -x), inv, q0);
+    return __fmaf_rn(-__fmaf_rn(q1, s, -x), inv, q1);
   };
   auto write = [&](const Pairs& x, int r) {
     float q[16];
