@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, d));
-        const int e = amax > 0.0f ? max((int)(__float_as_uint(amax) >> 23) - 127, -100) : 0;
+        const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100);
         // (0 where a value is infinite: its code becomes NaN, where a saturated one would make a finite score)
         const float mul = e == 128 ? 0.0f : __uint_as_float((uint32_t)(127 + 7 - e) << 23);
         if (c == 0) qscales[128 * wg + r] = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
