@@ -137,3 +137,13 @@ def test_attention_query_that_is_not_finite(Hq, add, k_exp, value):
     assert torch.isnan(got[add // 2, 1].float()).all()
     got[add // 2, 1] = plain[add // 2, 1]
     assert torch.equal(got, plain)
+
+
+@pytest.mark.parametrize("value", [0.0, 2.0 ** -120])
+@pytest.mark.parametrize("Hq,add", [(4, 1), (24, 1), (4, 130)])
+def test_attention_of_queries_without_size(Hq, add, value):
+    """Queries of zeros, or of values whose scores vanish: the mean of the values seen."""
+    rng = np.random.default_rng(Hq)
+    _, xq, cache, codes, scale, t = attention_case(rng, [500], [add], 16, Hq, 1, 128)
+    xq = np.full(xq.shape, value, np.float32)
+    check_attention(torch.from_numpy(xq).to(torch.bfloat16).cuda(), xq, cache, codes, scale, t, add)
