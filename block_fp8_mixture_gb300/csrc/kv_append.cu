@@ -9,8 +9,9 @@
 // one warp, in prompts the warps that hold a page; four warps or more make a block.  The remaining blocks
 // rotate Q, a token each: a thread holds the cos and sin of 8 pairs (HALF: 8 values and the 8 at rot/2
 // from them) and applies them to every head it has.
-// Prompts of 8331 tokens, 32 + 2 x 8 heads of 128: 40.5 us, 4.74 TB/s, 70% of the measured copy rate
-// (rotated rows kept: 53 us; eight rows a thread: 63 us).  32 single tokens: 3.6 us, 253: 7.5 us, latency.
+// Prompts of 8331 tokens, 32 + 2 x 8 heads of 128: 40.7 us as a graph (43.0 back to back from Python), 4.7 TB/s,
+// 70% of the measured copy rate (rotated rows kept: 53 us; eight rows a thread: 63 us).  32 single tokens: 3.2 us,
+// 253: 7.1 us, latency.
 #include <algorithm>
 
 #include "kv_device.cuh"

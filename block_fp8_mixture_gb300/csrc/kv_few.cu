@@ -9,8 +9,9 @@
 //   O^T[d][row]     = sum_token V[token][d] P[row][token]   A = V tile, MN-major
 // What is not 8-bit is split into E4M3 terms on the N side, each with its own column, which keeps the
 // accumulation in fp32 and costs no second read of A: a row of Q, scaled by a power of two, into
-// two terms (the second x 32: 8 bits, absolute error 2^-15 of the largest value), a row of P into
-// three (x 1, x 32, x 1024: 12 bits down to 2^-13 of the running maximum, 8 at 2^-17, 4 at 2^-21).
+// two terms (the second x 32: 8 bits, absolute error 2^-15 of the largest value), a row of P, rounded to
+// FP16 first, into three (x 1, x 32, x 1024: 11 bits down to 2^-13 of the running maximum, 8 at 2^-17, 4 at
+// 2^-21, nothing below 2^-25).
 // The page's K scale multiplies the score.  Its V scale goes into the exponent: with f = K scale x softmax
 // scale and lv = log2 V scale, p' = 2^(s f + lv - M), where M is the row's running maximum of s f + lv.  Then
 // O = sum p' code needs no scale, the row sum is sum p' / V scale, and the terms keep their bits however far
@@ -29,10 +30,11 @@
 // The maximum that scores are taken relative to moves only when one passes it by 8 x (2^3): then
 // all threads of the warpgroup reduce the tile's maximum and rescale, else a vote is all it costs.
 //
-// 128 requests of 8k to 16k tokens, 64 / 8 heads of 128: 447 us, 6.85 TB/s, at the measured copy rate (6.77).
-// 32 / 8 heads, one request of 128k: 53 us, 5.1 TB/s; of 4k: 11 us, of which start and join are 9.  61 of 6
-// to 8190 tokens, 40 / 8 heads: 38 us, 4.0 TB/s.  Heads of 64: 5.1 TB/s at best, a tile's chain of scores,
-// softmax and product takes longer than its bytes (three CTAs an SM instead of two: registers spill, 102 -> 108 us).
+// 128 requests of 8k to 16k tokens, 64 / 8 heads of 128: 445 to 452 us from box to box, 6.8 TB/s, at the measured
+// copy rate (6.77).  32 / 8 heads, one request of 128k: 53 us, 5.0 TB/s; of 4k: 11 us, of which start and join are
+// 9.  61 of 6 to 8190 tokens, 40 / 8 heads: 38 us, 4.0 TB/s.  Heads of 64: 5.2 TB/s at best, a tile's chain of
+// scores, softmax and product takes longer than its bytes (three CTAs an SM instead of two: registers spill, 102 ->
+// 108 us).
 #include <algorithm>
 
 #include "kv_plan.cuh"
@@ -946,7 +948,7 @@ __global__ void __launch_bounds__(FewCfg<kD, kNR>::Threads, FewCfg<kD, kNR>::Cta
 // cost softmax time whether they are live or not, so the fewest that hold them win: 64 x 4000 tokens, 4 rows
 // live, 8 / 16 / 32 / 64 rows: 89 / 90 / 120 / 235 us; 40 x 4000, 16 live: 42 / 51 / 89 us from 16 on.
 // More than 64 rows are the prompt kernel's; up to 64 this one is faster (32 rows, 32 x 4000: 44 against
-// 114 us; 64 rows, 32 x 8000: 130 against 198 us), and at 72 and 96 the prompt kernel costs what it does at 64.
+// 114 us; 64 rows, 32 x 8000: 121 against 198 us), and at 72 and 96 the prompt kernel costs what it does at 64.
 int few_rows(int G, int max_q) {
   const long long r = (long long)G * max_q;
   const long long rows = r <= 64 ? r : G;   // prompts: the single tokens among them still come here

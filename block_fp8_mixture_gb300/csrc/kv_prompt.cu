@@ -24,11 +24,12 @@
 // Work: rounds over the blocks, longest first, and a last one whose tiles are poured over the pairs up to
 // a common level (kv_plan.cuh).  Blocks that this cuts along the cache k_prompt_join adds up, in order.
 //
-// 4096 tokens after 28000, 32 / 8 heads of 128: 1.30 ms, 1.55 PFLOP/s, 82% of the measured 16-bit rate.  At
-// 1.42 ms the other layouts took: one CTA per block of 256 rows 1.59 ms; V read past shared memory 1.72 ms;
+// 4096 tokens after 28000, 32 / 8 heads of 128: 1.31 ms in a short burst, 1.54 PFLOP/s, 81% of the measured
+// 16-bit rate; 1.34 to 1.36 ms back to back, where the power cap holds the clock.  At 1.42 ms the other layouts
+// took: one CTA per block of 256 rows 1.59 ms; V read past shared memory 1.72 ms;
 // two threads a row 1.52 ms; an issuing warp per tile of rows 1.85 ms.  A step of 512 rows x 128 tokens takes
 // about 3300 cycles, of which the products need 2050: what is left is the chain score -> softmax -> product
-// of each tile.  Five prompts of 300 to 4000 tokens: 175 us, 1.03 PFLOP/s, the start and end of each block
+// of each tile.  Five prompts of 300 to 4000 tokens: 174 us, 1.04 PFLOP/s, the start and end of each block
 // being about 2.5 steps.
 #include <algorithm>
 
@@ -56,8 +57,9 @@ struct PromptCfg {
   static constexpr int Smem = 1024 + Tiles + 8 * OutWarp + 1024 + Slots * 128 + Works * 64 + kCtaRows * 4;
   // A part of a cut block: a row's values as FP32 without the last 8 bits, four in three words, and the
   // row's maximum and sum.  The join adds in FP32; what is left off, 2^-15 of a part's value, is a 128th of
-  // the output's own rounding to BF16.  (FP16 with a scale per row is a 2^-11: seen in single values where large
-  // parts cancel.)
+  // the output's own rounding to BF16.  Whole FP32 values would cost a third more traffic, and 42 instead of 32 MB
+  // of workspace at heads of 128.  (FP16 with a scale per row is a 2^-11: seen in single values where large parts
+  // cancel.)
   static constexpr int PartWords = kCtaRows * (kD * 3 / 4 + 2);
 };
 

@@ -137,7 +137,11 @@ moe_status moe_rope_append(const moe_rope_append_args* args, moe_stream_t stream
  * j > p - window.  out = sum_j softmax_j(sm_scale * q . k_j) v_j per head; head h reads key/value head
  * h / (Hq / Hkv).  A row that sees nothing (kv_len[b] < n, or kv_len[b] = 0) is zero.  Rows of q past
  * tok_start[B] are neither read nor written.
- * Scores, softmax statistics and sums are fp32; out is rounded once to BF16.
+ * Scores, softmax statistics and sums are fp32; out is rounded once to BF16.  On the way into the matrix
+ * products a row of q is rounded to 2^-15 of its largest value (2^-17 with many query rows), and a probability
+ * times the V scale of its page to 11 bits, down to 2^-13 of the largest of its row; from there the error is
+ * absolute, at most 2^-25 of that largest one (2^-29 with many query rows).
+ * Scales are not negative; a V scale below 1e-30 counts as 1e-30.
  * A row that sees something and whose q holds an infinity or a NaN is NaN.
  * max_q is an upper bound of the n (requests with more tokens are cut to max_q tokens by the caller's
  * mistake: their later rows are left unwritten).
