@@ -51,9 +51,14 @@ __device__ __forceinline__ Pair pair_mul(const Pair& a, const Pair& b) {
 }
 
 // exp(x) for x <= 0: x = k ln 2 + 16 m, |m| <= 0.0217; exp(m) - 1 by its power series, whose terms from m^4 on are
-// small enough for fp32; then four times (1 + e)^2 = 1 + (2 e + e^2).
-__device__ __forceinline__ Pair pair_exp(const Pair& x) {
-  if (!(x.hi > -200.0f)) return {0.0f, 0.0f};
+// small enough for fp32; then four times (1 + e)^2 = 1 + (2 e + e^2).  The power of two stays apart: a small pair would have
+// no room for its low word.
+struct Scaled {
+  Pair m;      // exp(x - k ln 2), from 0.7 to 1.42, or zero
+  int k;       // the value is m 2^k
+};
+__device__ __forceinline__ Scaled pair_exp(const Pair& x) {
+  if (!(x.hi > -200.0f)) return {{0.0f, 0.0f}, 0};
   const float k = rintf(x.hi * 1.44269504f);
   Pair m = {x.hi - k * kLn2a, x.lo};
   const float q = k * kLn2b;
@@ -74,14 +79,22 @@ __device__ __forceinline__ Pair pair_exp(const Pair& x) {
     pair_add(e, s);
   }
   pair_add(e, 1.0f);
-  const float a = ldexpf(1.0f, (int)k / 2), b = ldexpf(1.0f, (int)k - (int)k / 2);
-  return {e.hi * a * b, e.lo * a * b};
+  return {e, (int)k};
 }
 
-__device__ __forceinline__ float pair_div(const Pair& a, const Pair& b) {
-  const float q = a.hi / b.hi;
-  const float rest = __fmaf_rn(-q, b.hi, a.hi) + (a.lo - q * b.lo);
-  return q + rest / b.hi;
+// The value itself, for a sum with numbers about one: what a small one loses is far below that sum's low word.
+__device__ __forceinline__ Pair value_of(const Scaled& e) {
+  const float a = ldexpf(1.0f, e.k / 2), b = ldexpf(1.0f, e.k - e.k / 2);
+  return {e.m.hi * a * b, e.m.lo * a * b};
+}
+
+// a / b rounded once, for b from 1 to 1024.  Below 2^-126 fp32 keeps fewer bits, so a quotient that may lie there is
+// joined and scaled in 64 bits, and the conversion rounds it.
+__device__ __forceinline__ float pair_div(const Scaled& a, const Pair& b) {
+  const float q = a.m.hi / b.hi;
+  const float rest = (__fmaf_rn(-q, b.hi, a.m.hi) + (a.m.lo - q * b.lo)) / b.hi;
+  if (a.k > -100) return (q + rest) * ldexpf(1.0f, a.k);
+  return __double2float_rn(((double)q + (double)rest) * __hiloint2double((1023 + a.k) << 20, 0));
 }
 
 // ------------------------------------------------------------------------------------- the row
@@ -189,10 +202,10 @@ __device__ __noinline__ float exact_score(float x, bool softmax, float top, Pair
     pair_add(d, -top);
     return pair_div(pair_exp(d), total);
   }
-  const Pair e = pair_exp(Pair{-fabsf(x), 0.0f});
-  Pair one = e;
+  const Scaled e = pair_exp(Pair{-fabsf(x), 0.0f});
+  Pair one = value_of(e);
   pair_add(one, 1.0f);
-  return pair_div(x < 0.0f ? e : Pair{1.0f, 0.0f}, one);
+  return pair_div(x < 0.0f ? e : Scaled{{1.0f, 0.0f}, 0}, one);
 }
 
 // The sum of exp(x - top) over the warp's logits, `have` of them a lane, 32 words apart.
@@ -203,7 +216,7 @@ __device__ __noinline__ Pair exact_sum(const uint32_t* xs, int have, float top) 
     Pair d = {__uint_as_float(xs[32 * i]), 0.0f};
     if (d.hi > -INFINITY) {
       pair_add(d, -top);
-      pair_add(total, pair_exp(d));
+      pair_add(total, value_of(pair_exp(d)));
     }
   }
   return pair_reduce(total, 32);

@@ -1,0 +1,60 @@
+"""GPU: routing of values far from one, against the CPU statement in 64 bits.
+
+The kernels carry some 40 bits up to the roundings that the header names, so experts equal the statement's but where that
+stands within 2^-40 of a border between two scores.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import step_ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+import block_fp8_mixture_gb300 as moe  # noqa: E402
+from test_gpu_kv import dev  # noqa: E402
+
+
+@pytest.fixture(autouse=True)
+def _library():
+    moe.load_library(build_if_missing=True)
+
+
+def check(x, k, rel, bias=None, scale=1.0, **kw):
+    """ids to the bit; weights within rel of their value, and half of fp32's smallest step."""
+    ids, weights = moe.route(dev(x), k, bias=None if bias is None else dev(bias), scale=scale, **kw)
+    want, w = step_ref.route(x, k, bias=bias, scale=scale, **{"groups" if a == "num_groups" else a: b for a, b in kw.items()})
+    assert np.array_equal(ids.cpu().numpy(), want)
+    got = weights.cpu().numpy().astype(np.float64)
+    assert (np.abs(got - w) <= rel * np.abs(w) + 2.0 ** -150).all()
+
+
+def test_route_order_of_neighbours_with_small_scores():
+    """Scores that both round to 4.964734e-38; two of 22 bits; each pair once in either order."""
+    for row in ([0.10412609577, 0.10412610322, 86.0], [0.0, -0.27704, -0.164926, -95.027985, -95.02769]):
+        x = np.float32([row, row[::-1]])
+        check(x, len(row), 2.0 ** -18)
+
+
+@pytest.mark.parametrize("scoring", [0, 1])
+@pytest.mark.parametrize("G", [1, 4])
+def test_route_order_of_small_scores(scoring, G):
+    """A few logits at the top and pairs some 2^-11 to 2^-24 apart far below, so that the choice hangs on how scores round that
+    are small, or below fp32's normal numbers."""
+    rng = np.random.default_rng(7 + G)
+    M, E = 4000, 32
+    x = np.repeat(rng.uniform(-104, -70, (M, E // 2)), 2, 1)
+    x[:, ::2] += rng.choice([2.0 ** -16, 2.0 ** -13, 2.0 ** -11, 2.0 ** -9], (M, E // 2))
+    if scoring == 0:
+        x[:, ::8] = rng.uniform(-1, 0, (M, 4))          # one in each group, so that a group's value is one of these
+    x = x.astype(np.float32)
+    kw = dict(scoring=scoring, num_groups=G, topk_groups=G)
+    check(x, 16, 2.0 ** -18, renormalize=False, **kw)
+    check(x, 16, 2.0 ** -18, **kw)
+    check(x, 16, 2.0 ** -18, bias=np.zeros(E, np.float32), **kw)
+    if G > 1:
+        check(x, 10, 2.0 ** -18, scoring=scoring, num_groups=G, topk_groups=2)
