@@ -566,7 +566,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) k_route(const __grid_constan
   for (int d = 8; d >= 1; d >>= 1) total += __shfl_xor_sync(kAllLanes, total, d);
   if (lane < a.topk) {
     float w = s;
-    if (a.renormalize) w = total > 0.0f ? __fdividef(w, total) : 0.0f;
+    // (an approximate division's bounds end at divisors of 2^-126; sums of small sigmoids lie below)
+    if (a.renormalize) w = total > 0.0f ? __fdiv_rn(w, total) : 0.0f;
     w *= a.scale;
     if (spoilt) w = __int_as_float(0x7FC00000);
     const int64_t at = row * a.topk + lane;

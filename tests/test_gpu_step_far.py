@@ -58,3 +58,22 @@ def test_route_order_of_small_scores(scoring, G):
     check(x, 16, 2.0 ** -18, bias=np.zeros(E, np.float32), **kw)
     if G > 1:
         check(x, 10, 2.0 ** -18, scoring=scoring, num_groups=G, topk_groups=2)
+
+
+# Scores below 2^-104 that equal the statement's: what joins them are 4 additions over the lanes, a division and a product,
+# 2^-24 of the value each.
+FEW = 6 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("k", [1, 3, 8, 16])
+def test_route_renormalizes_small_sums(bias, k):
+    """Sigmoid scores whose sum is below fp32's normal numbers: weights are still shares of it."""
+    rng = np.random.default_rng(k)
+    x = rng.uniform(-103.5, -91, (500, 48)).astype(np.float32)
+    x[0], x[1] = -103.0, -92.0
+    x[2, 1:] = -200.0
+    x[3] = -200.0
+    b = (rng.integers(0, 4, 48) / 8).astype(np.float32) if bias else None
+    check(x, k, FEW, bias=b, scoring=1)
+    check(x, k, FEW, bias=b, scoring=1, scale=2.5)
