@@ -489,16 +489,18 @@ __global__ void __launch_bounds__(32 * kRouteWarps) k_route(const __grid_constan
 
   // their scores and keys, and how far off those may be
   int id = (int)found[lane];
-  float s = 0.0f, key = -INFINITY, off = 0.0f, logit = -INFINITY;
+  float s = 0.0f, key = -INFINITY, off = 0.0f, logit = -INFINITY, depth = -INFINITY;   // depth: the score is at most its exp
   if (id >= 0) {
     logit = logit_of(id);
     if (kSoftmax) {
       Pair d = {logit, 0.0f};
       pair_add(d, -top);
       s = exp_of(d.hi) * (1.0f + d.lo) * inv;
+      depth = d.hi;
     } else {
       const float e = exp_of(-fabsf(logit));
       s = (logit < 0.0f ? e : 1.0f) * fast_rcp(1.0f + e);
+      depth = logit;
     }
     key = a.bias != nullptr ? s + a.bias[id] : s;
     // with a bias: 7 units of 2^-24 in the score, what the softmax's sum is off, the key's rounding
@@ -512,6 +514,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) k_route(const __grid_constan
     const bool last = lane == a.topk - 1;
     const float bound = rest <= kNever ? -INFINITY : key_of(rest | kPlace);
     if (a.bias != nullptr) {
+      // a score near fp32's smallest numbers weighs as its few bits say: it is evaluated again, unless it is zero for sure
+      unsure |= s < 1e-36f && depth > -105.0f;
       unsure |= !(key - (last ? bound : next_key) > off + (last ? off + slack : next_off));
     } else {
       // rounded scores keep the order of logits; they differ where the scores are more than 2^-23 of them apart, and

@@ -77,3 +77,19 @@ def test_route_renormalizes_small_sums(bias, k):
     b = (rng.integers(0, 4, 48) / 8).astype(np.float32) if bias else None
     check(x, k, FEW, bias=b, scoring=1)
     check(x, k, FEW, bias=b, scoring=1, scale=2.5)
+
+
+@pytest.mark.parametrize("scoring", [0, 1])
+@pytest.mark.parametrize("G", [1, 4])
+def test_route_weights_of_small_scores_that_a_bias_chose(scoring, G):
+    """The bias chooses experts whose scores have few bits left, or none: their weights are shares of those scores."""
+    rng = np.random.default_rng(3)
+    x = rng.uniform(-106, -86, (600, 64)).astype(np.float32)
+    b = (np.arange(64) % 16 / 16).astype(np.float32)
+    x[:, 16 * np.arange(4)] = 1.0                        # the top of the softmax, which no bias helps
+    b[16 * np.arange(4)] = -3.0
+    x[5, 1::2] = -1e4                                    # finite masks
+    kw = dict(scoring=scoring, bias=b, num_groups=G, topk_groups=G)
+    check(x, 8, FEW, **kw)
+    check(x, 8, FEW, renormalize=False, **kw)
+    check(x, 12, FEW, scale=0.75, **kw)
