@@ -23,8 +23,9 @@ extern "C" {
  * Per live row of H values:
  *   h = RN_bf16(x + residual), or x where residual is NULL; h is written to residual_out
  *   y = RN_bf16(RN_fp32(h * w * (mean(h^2) + eps)^-1/2)), w = weight, or RN_fp32(1 + weight) with weight_plus_one
- * Squares, their sum, the root and the products carry at least 40 bits up to the one rounding to fp32, so y
- * does not depend on how a row is split over threads.
+ * Squares, their sum, the root and the products carry some 40 bits up to the one rounding to fp32, so y
+ * does not depend on how a row is split over threads.  (Fewer where y is below 2^-100, or h below that share of the root.)
+ * Weights are finite; h * w may leave fp32's range where y does not.
  *   out     y itself (NULL: not wanted)
  *   codes, scales: y quantized per 1x128 group exactly as moe_quant_act quantizes such a row, with its formats
  *           and numerics (NULL: not wanted).  The last group is shorter where 128 does not divide H.

@@ -1,12 +1,14 @@
-"""GPU: routing of values far from one, against the CPU statement in 64 bits.
+"""GPU: norm and routing of values far from one, against the CPU statement in 64 bits.
 
-The kernels carry some 40 bits up to the roundings that the header names, so experts equal the statement's but where that
-stands within 2^-40 of a border between two scores.
+The kernels carry some 40 bits up to the roundings that the header names, so whole numbers and BF16 values equal the
+statement's but where that stands within 2^-40 of a border between two results.  Values are drawn a few million at a
+time, so that an error of 2^-28 before the rounding to BF16 (borders 2^-8 apart) shows in some of them.
 """
 
 import numpy as np
 import pytest
 
+import oracle
 from oracle import step_ref
 
 pytestmark = pytest.mark.gpu
@@ -17,6 +19,7 @@ if not torch.cuda.is_available():
 
 import block_fp8_mixture_gb300 as moe  # noqa: E402
 from test_gpu_kv import dev  # noqa: E402
+from test_gpu_step import same_bits  # noqa: E402
 
 
 @pytest.fixture(autouse=True)
@@ -93,3 +96,44 @@ def test_route_weights_of_small_scores_that_a_bias_chose(scoring, G):
     check(x, 8, FEW, **kw)
     check(x, 8, FEW, renormalize=False, **kw)
     check(x, 12, FEW, scale=0.75, **kw)
+
+
+# ------------------------------------------------------------------------------------------------ norm
+def norm(xv, w, eps, wide, **kw):
+    """The kernel's rows and the statement's."""
+    wt = dev(w) if wide else dev(w).to(torch.bfloat16)
+    got = moe.rms_norm(dev(xv).to(torch.bfloat16), wt, eps=eps, **kw).out
+    return got, step_ref.rms_norm(xv, w, eps)[0]
+
+
+def rows(rng, M, H, exponent):
+    return oracle.bf16_round((rng.standard_normal((M, H)) * 2.0 ** exponent).astype(np.float32))
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("H", [8, 264, 4096, 4100])
+def test_norm_of_far_products(wide, H):
+    """The value times its weight leaves fp32's range where the normed value does not."""
+    rng = np.random.default_rng(H)
+    w = oracle.bf16_round(rng.standard_normal(H).astype(np.float32))
+    for h_exponent, w_exponent, eps in ((50, 83, 1e-6), (66, 62, 1e-6), (30, 100, 1e-6), (120, 20, 1e-6), (-30, -95, 1e-20),
+                                        (-20, -80, 1e-6), (-60, -60, 1e-20)):
+        v = w * np.float32(2.0 ** w_exponent)
+        if wide:
+            v = (v * (1 + 2.0 ** -12 * rng.random(H))).astype(np.float32)
+        got, want = norm(rows(rng, 700, H, h_exponent), v, eps, wide)
+        assert np.isfinite(want).all()
+        same_bits(got, want)
+    got, _ = norm(np.full((2, H), 1e15, np.float32), np.full(H, 1e25, np.float32), 1e-6, True)
+    same_bits(got, np.full((2, H), oracle.bf16_round(np.float32([1e25]))[0]))
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_norm_of_results_beyond_the_largest_number(wide):
+    """Infinite where the value times its weight is, with the value's sign; finite beside it."""
+    w = np.full(64, 3e38, np.float32)
+    w[1::2] = -1.0
+    xv = rows(np.random.default_rng(0), 300, 64, 3)
+    got, want = norm(xv, oracle.bf16_round(w), 1e-6, wide)
+    assert np.isinf(want).any() and np.isfinite(want).any() and not np.isnan(want).any()
+    same_bits(got, want)
