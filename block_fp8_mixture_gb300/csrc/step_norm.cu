@@ -17,8 +17,10 @@ struct NormParams {
   float eps_hi, eps_lo;
 };
 
-// Squares of values above 2^63 leave fp32's range: such a row is summed again with h * 2^-76.
-constexpr float kSmaller = 1.3234889800848443e-23f;   // 2^-76
+// The root of s = mean(h^2) + eps needs its square, whose low word has no room from s = 2^100 on (and squares of values above 2^63
+// leave fp32's range): such a row is summed again with h * 2^-80, and eps * 2^-160.
+constexpr float kSmaller = 8.271806125530277e-25f;    // 2^-80
+constexpr float kLargest = 1.2676506002282294e30f;    // 2^100
 
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -308,7 +310,7 @@ k_rms_norm(const __grid_constant__ NormParams p) {
     for (int i = 0; i < VPT; ++i) h_edges[i * 32 + t / 32] = h[i];
   }
 
-  // the sum of squares, twice where it leaves fp32's range
+  // the sum of squares, twice where it or eps is large
   float scale = 1.0f;
   Pair sum;
 #pragma unroll 1
@@ -321,7 +323,7 @@ k_rms_norm(const __grid_constant__ NormParams p) {
       sum = t % 32 < warps ? part[pass][t % 32] : Pair{0.0f, 0.0f};
       sum = pair_reduce(sum, 32);
     }
-    if (sum.hi < INFINITY) break;
+    if (sum.hi < kLargest && p.eps_hi < kLargest) break;
     if (pass == 0) scale = kSmaller;
   }
 
@@ -329,10 +331,8 @@ k_rms_norm(const __grid_constant__ NormParams p) {
   Pair s;
   s.hi = sum.hi * p.inv_hi;
   s.lo = __fmaf_rn(sum.hi, p.inv_hi, -s.hi) + (sum.hi * p.inv_lo + sum.lo * p.inv_hi);
-  if (scale == 1.0f) {
-    pair_add(s, p.eps_hi);   // nothing beside squares above 2^126
-    s.lo += p.eps_lo;
-  }
+  pair_add(s, p.eps_hi * scale * scale);
+  s.lo += p.eps_lo * scale * scale;
   Pair r = {rsqrtf(s.hi), 0.0f};
   if (sum.hi < INFINITY) {
     const float q = r.hi * r.hi, q_lo = __fmaf_rn(r.hi, r.hi, -q);

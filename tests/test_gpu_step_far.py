@@ -137,3 +137,26 @@ def test_norm_of_results_beyond_the_largest_number(wide):
     got, want = norm(xv, oracle.bf16_round(w), 1e-6, wide)
     assert np.isinf(want).any() and np.isfinite(want).any() and not np.isnan(want).any()
     same_bits(got, want)
+
+
+@pytest.mark.parametrize("exponent", [40, 50, 56, 59, 61, 62])
+@pytest.mark.parametrize("wide", [False, True])
+def test_norm_of_large_rows_keeps_its_bits(exponent, wide):
+    """Sums of squares below fp32's largest number, whose root's square is near its smallest."""
+    rng = np.random.default_rng(exponent)
+    w = rng.standard_normal(8).astype(np.float32)
+    w = w if wide else oracle.bf16_round(w)
+    got, want = norm(rows(rng, 1 << 18, 8, exponent), w, 1e-6, wide)
+    same_bits(got, want)
+
+
+@pytest.mark.parametrize("eps", [1e20, 1e30, 1e36, 1e38, 3.4e38])
+@pytest.mark.parametrize("exponent", [0, 55, 62, 65, 70])
+def test_norm_of_a_large_eps(eps, exponent):
+    """eps counts in every row, whatever its values: in one whose squares leave fp32's range too."""
+    rng = np.random.default_rng(exponent)
+    w = rng.standard_normal(8).astype(np.float32)
+    xv = rows(rng, 1 << 17, 8, exponent)
+    same_bits(*norm(xv, w, eps, True))
+    xv = rows(rng, 9, 4096, exponent)
+    same_bits(*norm(xv, rng.standard_normal(4096).astype(np.float32), eps, True))
