@@ -302,7 +302,8 @@ class MoELayer:
     [E, 2I/128, H/128] (fp32, or uint8 UE8M0), w2 [E, H, I], s2 [E, H/128, I/128].
 
     Its input is x, bf16 [M, H], or rms_norm's result with quant = act_fmt (and the layer's numerics), whose codes
-    the layer then takes instead of quantizing the rows itself: the output is the same.
+    the layer then takes instead of quantizing the rows itself: the output is the same.  Codes of another format or other
+    numerics are refused.
     """
 
     def __init__(self, w13, s13, w2, s2, *, weight_fmt=SCALE_FP32, act_fmt=SCALE_FP32,
@@ -344,6 +345,10 @@ class MoELayer:
         import torch
         if x.codes is None:
             raise ValueError("the norm's result holds no codes (quant)")
+        # (scales that are powers of two are the same in both numerics)
+        if x.quant is not None and (x.quant != self.act_fmt or (x.quant == SCALE_FP32 and x.numerics != self.numerics)):
+            raise MoeError(MOE_ERR_INVALID_ARG, f"codes of quant={x.quant}, numerics={x.numerics}; the layer's are "
+                                                f"act_fmt={self.act_fmt}, numerics={self.numerics}")
         if x.codes.shape[0] > self.M_cap:
             raise ValueError(f"{x.codes.shape[0]} tokens exceed the layer's capacity {self.M_cap}")
         if out is None:

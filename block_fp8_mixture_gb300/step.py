@@ -61,12 +61,23 @@ SIGNATURES = {
 }
 
 
-class Normed(NamedTuple):
-    """rms_norm's outputs; those not asked for are None."""
+class _Outputs(NamedTuple):
     out: object        # bf16 [M, H]
     residual: object   # bf16 [M, H]
     codes: object      # float8_e4m3fn (or uint8) [M, H]
     scales: object     # [ceil(H / 128), M] fp32, or uint8 UE8M0
+
+
+class Normed(_Outputs):
+    """rms_norm's outputs; those not asked for are None.  quant and numerics say how the codes were made, so that a layer
+    can refuse those of another format; None where there are no codes, or a caller has put them together."""
+    quant = None
+    numerics = None
+
+    def _replace(self, **kw):
+        new = super()._replace(**kw)
+        new.quant, new.numerics = self.quant, self.numerics
+        return new
 
 
 class Verified(NamedTuple):
@@ -146,7 +157,10 @@ def rms_norm(x, weight, *, eps: float = 1e-6, residual=None, residual_out=None, 
     a = _PACK_NORM.pack(xp, rp, wp, _count(d_num_tokens, d), rop, op, cp, sp, xs, rs, ros, os, cs, ss, eps, M, H,
                         wide, bool(weight_plus_one), quant or 0, numerics)
     _check(load_library().moe_rms_norm(a, _stream(stream, d)), "moe_rms_norm")
-    return Normed(out, residual_out, codes, scales)
+    got = Normed(out, residual_out, codes, scales)
+    if quant is not None:
+        got.quant, got.numerics = quant, numerics
+    return got
 
 
 def _codes(codes, scales, act_fmt: int, dev: int):
