@@ -82,10 +82,17 @@ __device__ __forceinline__ Scaled pair_exp(const Pair& x) {
   return {e, (int)k};
 }
 
-// The value itself, for a sum with numbers about one: what a small one loses is far below that sum's low word.
+__device__ __forceinline__ float power_of_two(int k) { return __int_as_float((127 + k) << 23); }   // k from -126 on
+
+// The value itself, for a sum of at least one: what a small one loses is far below that sum's low word.
 __device__ __forceinline__ Pair value_of(const Scaled& e) {
-  const float a = ldexpf(1.0f, e.k / 2), b = ldexpf(1.0f, e.k - e.k / 2);
-  return {e.m.hi * a * b, e.m.lo * a * b};
+  const float a = power_of_two(max(e.k, -126));
+  return {e.m.hi * a, e.m.lo * a};
+}
+
+// (In line, its registers spill in the kernel of two experts a lane.)
+__device__ __noinline__ float small_quotient(float q, float rest, int k) {
+  return __double2float_rn(((double)q + (double)rest) * __hiloint2double((1023 + k) << 20, 0));
 }
 
 // a / b rounded once, for b from 1 to 1024.  Below 2^-126 fp32 keeps fewer bits, so a quotient that may lie there is
@@ -93,8 +100,8 @@ __device__ __forceinline__ Pair value_of(const Scaled& e) {
 __device__ __forceinline__ float pair_div(const Scaled& a, const Pair& b) {
   const float q = a.m.hi / b.hi;
   const float rest = (__fmaf_rn(-q, b.hi, a.m.hi) + (a.m.lo - q * b.lo)) / b.hi;
-  if (a.k > -100) return (q + rest) * ldexpf(1.0f, a.k);
-  return __double2float_rn(((double)q + (double)rest) * __hiloint2double((1023 + a.k) << 20, 0));
+  if (a.k > -100) return (q + rest) * power_of_two(a.k);
+  return small_quotient(q, rest, a.k);
 }
 
 // ------------------------------------------------------------------------------------- the row
