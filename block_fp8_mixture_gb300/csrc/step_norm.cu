@@ -10,7 +10,7 @@ namespace moe {
 // other side of a BF16 border from a 64-bit evaluation, and a group's scale with its largest value.
 // What that takes, some 20 operations a value, is done two values at a time (fp32x2): one at a time, with divisions for the
 // codes, 8192 x 7168 with residual and 8-bit form took 172 us.  It takes 85 us, 6.2 TB/s, where a copy runs at 6.7 (without
-// the 8-bit form 69 us, 6.75 TB/s).  Few rows are all latency: 1 x 4096 2.2 us, 32 x 4096 with the 8-bit form 2.7 us.
+// the 8-bit form 69 us, 6.8 TB/s).  Few rows are all latency: 1 x 4096 2.3 us, 32 x 4096 with the 8-bit form 2.7 us.
 struct NormParams {
   moe_rms_norm_args a;
   float inv_hi, inv_lo;   // 1 / H
@@ -269,7 +269,7 @@ __device__ __forceinline__ uint2 codes8(const uint4& y, const GroupScale& g) {
 }
 
 // Threads of a block at most: 72 registers a thread let four blocks of 224 with four vectors a thread share an SM (8192 x
-// 7168 without the 8-bit form: 69 us, with 84 registers 91 us; 8192 x 7167: 116 us, with 102 registers 157 us).
+// 7168 without the 8-bit form: 69 us, with 84 registers 91 us; 8192 x 7167: 114 us, with 102 registers 157 us).
 __host__ __device__ constexpr int most_threads(int vpt) { return vpt <= 2 ? 1024 : vpt == 4 ? 448 : 512; }
 
 // VPT vectors a thread.  kWarpRows: a row a warp, four of them a block; otherwise a row a block of any number of warps.

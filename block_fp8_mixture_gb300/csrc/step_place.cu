@@ -5,7 +5,7 @@ namespace moe {
 
 // Each token's codes and scales go to the workspace rows of its live pairs: what k_quant_act does behind its
 // quantization.  A thread moves 16 codes; the eight of a group share its scale.  Bound by HBM: H + 4 H / 128 bytes a token read,
-// topk times as many written: 4096 x 7168 for 8 experts each 47 us, 5.6 TB/s (quantizing the BF16 rows 53 us).
+// topk times as many written: 4096 x 7168 for 8 experts each 47 us, 5.8 TB/s (quantizing the BF16 rows 54 us).
 constexpr int kPlaceThreads = 256;
 constexpr int kPlaceBytes = 16;
 

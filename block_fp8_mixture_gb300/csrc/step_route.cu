@@ -9,8 +9,8 @@ namespace moe {
 // the row again with exponentials of some 2^-45 (pairs of fp32 words: 64-bit arithmetic runs at a sixty-fourth of the rate).
 //
 // What bounds it is the number of operations, half of them on the integer and comparison pipe: about 700 a row of 256 experts
-// in groups, 8 chosen (some 250 of them whatever E and k, 130 for groups, 13 for each choice).  16384 such rows 14.1 us (the
-// bytes alone: 2.7), 8192 BF16 rows of 128 experts 5.3 us, one row 2.5 us; all scores in 64 bits took 214, 60 and 11 us.
+// in groups, 8 chosen (some 250 of them whatever E and k, 130 for groups, 15 for each choice).  16384 such rows 14.1 us (the
+// bytes alone: 2.7), 8192 BF16 rows of 128 experts 5.4 us, one row 2.6 us; all scores in 64 bits took 214, 60 and 11 us.
 //
 // A warp a token.  Its lanes are dealt to the groups (L = 32 / groups a group, rounded down to a power of two) and hold
 // consecutive experts, lower ids in higher lanes, so a group's statistics need shuffles among its lanes only.
@@ -494,7 +494,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) k_route(const __grid_constan
   const uint32_t rest = __reduce_max_sync(kAllLanes, head & ~kPlace);     // of all that are left
   __syncwarp();
 
-  // their scores and keys, and how far off those may be
+  // Their scores and keys, and how far off those may be.  Weights come of these scores unless the row is evaluated again: off by
+  // 1.1 units of 2^-24 in the mean square; with expf and true divisions in their place by 1.1 too, in the same time.
   int id = (int)found[lane];
   float s = 0.0f, key = -INFINITY, off = 0.0f, logit = -INFINITY, depth = -INFINITY;   // depth: the score is at most its exp
   if (id >= 0) {

@@ -82,7 +82,8 @@ moe_status moe_fp8_block_forward_codes(const moe_fwd_args* args, const void* cod
  *   topk_ids: the experts of the topk largest keys, in descending order, the lower id first among equals.
  *   topk_weights: s of those (not the key); with renormalize divided by their sum (0 where the sum is 0); times scale.
  * Keys are compared as if they had been computed exactly and rounded as above: the choice is that of a 64-bit
- * evaluation but where that itself stands within 2^-40 of a rounding border.  Weights are within 2^-18 of their value.
+ * evaluation but where that itself stands within 2^-38 of a rounding border.  Weights are within 2^-18 of their value, where
+ * the bounds of all that approximates add up; some 2^-24 as a rule, as with every part of them rounded to fp32.
  * An expert whose logit is -inf (a mask), or whose key is -inf or NaN, is never chosen, nor a group without any
  * other.  Places that find no expert get id -1 and weight 0 (the layer drops such pairs).  A NaN logit, and with
  * MOE_ROUTE_SOFTMAX a logit of +inf, is never chosen and makes all the row's weights NaN.
@@ -118,9 +119,10 @@ moe_status moe_route(const moe_route_args* args, moe_stream_t stream);
  *   The token after them has the distribution r: max(target - draft, 0) of row a where its draft was refused
  *   (fp32 difference; with certain drafts target without the drafted token), target of row n - 1 where all were
  *   accepted; target of row a where nothing is left of r.  It is the first token whose cumulative sum of r
- *   exceeds uniform_next[b] times the sum of r, with sums in at least 45 bits.
+ *   exceeds uniform_next[b] times the sum of r, with sums in pairs of fp32 words, some 45 bits (a place within
+ *   2^-32 of the sum beside a border between two tokens may fall to either).
  * Entries that are NaN or not above zero count as zero.  Rows need not sum to exactly one.
- *   accepted[b] = a;  next_token[b] = the token, -1 where r is zero throughout or its sum is infinite
+ *   accepted[b] = a;  next_token[b] = the token, -1 where r is zero throughout or its sum leaves fp32's range
  *   kept_len[b] = kv_len[b] - n + a + 1: the cached tokens that stay (the length to take the cache back to)
  * A request without rows gets 0, -1, kv_len[b]; so does one whose first row's slot is -1 (slot not NULL: the
  * step's tables refused it).  uniform and uniform_next are in [0, 1); what is not counts as the nearest end
